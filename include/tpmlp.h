@@ -50,8 +50,9 @@ typedef enum tpmlp_status {
 } tpmlp_status;
 
 /* Element type of X, A, a, B, b, H, Y, Z, dZ, dH and dX. Weight and bias
- * gradients (dA, da, dB, db) are always fp32 ("weight update in full
- * precision", page "Megatron", section "其他关键技术 / 混合精度训练").
+ * gradients (dA, da, dB, db) are fp32 ("weight update in full precision",
+ * page "Megatron", section "其他关键技术 / 混合精度训练"), except where an
+ * entry point takes their type as an argument.
  * TPMLP_BF16 accumulates in fp32 on the tensor cores; TPMLP_FP32 uses fp32
  * FFMA throughout (no TF32). */
 typedef enum tpmlp_dtype { TPMLP_BF16 = 0, TPMLP_FP32 = 1 } tpmlp_dtype;
@@ -60,7 +61,11 @@ typedef enum tpmlp_dtype { TPMLP_BF16 = 0, TPMLP_FP32 = 1 } tpmlp_dtype;
  * tp_mlp_fwd and tp_mlp_bwd use (the pages name the activation only as
  * "gelu"). TPMLP_GELU_TANH is the tanh approximation
  * ½·x·(1 + tanh(√(2/π)·(x + 0.044715·x³))) (Hendrycks & Gimpel, 2016). */
-typedef enum tpmlp_activation { TPMLP_GELU_ERF = 0, TPMLP_GELU_TANH = 1 } tpmlp_activation;
+typedef enum tpmlp_activation {
+    TPMLP_GELU_ERF = 0,
+    TPMLP_GELU_TANH = 1,
+    TPMLP_ACT_NONE = 2 /* the identity; tp_linear_fwd_ex and tp_linear_bwd_ex only */
+} tpmlp_activation;
 
 /* Bytes of device workspace that tp_mlp_fwd and tp_mlp_bwd need for these
  * sizes under the current split policy and dynamic-schedule setting (the
@@ -151,6 +156,66 @@ tpmlp_status tp_linear_bwd(const void* dY, const void* X, const void* W, void* d
                            float* dbias, int64_t T, int64_t K, int64_t N, int p, tpmlp_split split,
                            tpmlp_dtype dt, void* workspace, size_t workspace_bytes, void* stream);
 
+/* The linear layer with its activation and a residual in the product's
+ * epilogue: H = X·W + bias, Y = act(H) + R. Arguments as tp_linear_fwd, plus:
+ * act: TPMLP_ACT_NONE, TPMLP_GELU_ERF or TPMLP_GELU_TANH.
+ * R: T×N of dtype dt, added after the activation, or NULL. R may be Y itself
+ *   (the residual stream updated in place); no other output may overlap an
+ *   input.
+ * H: T×N output of dtype dt, the pre-activation the backward needs, or NULL
+ *   (inference). With TPMLP_ACT_NONE it must be NULL.
+ * Up to 64 rows (single tokens, small batches) the tensor-core path splits K
+ * over a cluster of CTAs, so that reading W uses the whole GPU.
+ *
+ * Backward, for the upstream gradient dY (T×N; R's gradient is dY itself):
+ *   dH = dY ⊙ act′(H)        (T×N, dtype dt, rounded once; written to dH)
+ *   dbias = 1ᵀ·dH            (N, summed in fp32 before dH is rounded)
+ *   dW = Xᵀ·dH, dX = dH·Wᵀ   (from the stored dH)
+ * With TPMLP_ACT_NONE, dH is dY: H and dH must be NULL. dW and dbias have the
+ * type grad_dt: TPMLP_FP32, or dt for gradients held in the weights' type.
+ * Both calls need tpmlp_linear_ex_workspace_size() bytes of workspace (the
+ * larger of the two calls' needs; 0 for invalid sizes). With T == 0, dW and
+ * dbias are set to zero. */
+size_t tpmlp_linear_ex_workspace_size(int64_t T, int64_t K, int64_t N, int p, tpmlp_split split,
+                                      tpmlp_dtype dt);
+tpmlp_status tp_linear_fwd_ex(const void* X, const void* W, const void* bias, const void* R, void* H,
+                              void* Y, int64_t T, int64_t K, int64_t N, int p, tpmlp_split split,
+                              tpmlp_dtype dt, tpmlp_activation act, void* workspace,
+                              size_t workspace_bytes, void* stream);
+tpmlp_status tp_linear_bwd_ex(const void* dY, const void* X, const void* W, const void* H, void* dX,
+                              void* dW, void* dbias, void* dH, int64_t T, int64_t K, int64_t N, int p,
+                              tpmlp_split split, tpmlp_dtype dt, tpmlp_dtype grad_dt,
+                              tpmlp_activation act, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+/* Layer norm over the h columns of each row (the block's input in a pre-norm
+ * Transformer layer):
+ *   mean = Σ x / h,  var = Σ (x − mean)² / h,  rstd = 1/√(var + eps)
+ *   Y = (X − mean)·rstd ⊙ gamma + beta
+ * X, Y: T×h; gamma, beta: h, NULL for ones and zeros; all of dtype dt. mean,
+ * rstd: T floats each, kept for the backward, or both NULL. All sums are
+ * fp32, the variance around the mean (not E[x²] − mean²); Y is rounded once.
+ * h ≥ 1, eps ≥ 0 and finite. Pointers need the alignment of their element
+ * type only; rows whose start is 16-byte aligned are read 16 bytes at a time.
+ *
+ * Backward, for the upstream gradient dY and the forward's X, mean and rstd:
+ *   x̂ = (X − mean)·rstd,  g = dY ⊙ gamma
+ *   dX = rstd·(g − Σ g / h − x̂·Σ (g ⊙ x̂) / h) + dR
+ *   dgamma = Σ_rows dY ⊙ x̂,  dbeta = Σ_rows dY          (h, fp32)
+ * dR (T×h of dtype dt, or NULL) is the gradient that arrives along the
+ * residual path around the block; adding it here saves a pass over dX. The
+ * rows are summed in a fixed order. Needs tpmlp_layernorm_workspace_size()
+ * bytes (0 for invalid sizes). With T == 0, dgamma and dbeta are set to zero.
+ * No output may overlap an input, except that dX may be dY or dR itself. */
+size_t tpmlp_layernorm_workspace_size(int64_t T, int64_t h, tpmlp_dtype dt);
+tpmlp_status tp_layernorm_fwd(const void* X, const void* gamma, const void* beta, void* Y, float* mean,
+                              float* rstd, int64_t T, int64_t h, float eps, tpmlp_dtype dt,
+                              void* stream);
+tpmlp_status tp_layernorm_bwd(const void* dY, const void* X, const void* gamma, const float* mean,
+                              const float* rstd, const void* dR, void* dX, float* dgamma,
+                              float* dbeta, int64_t T, int64_t h, tpmlp_dtype dt, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
 /* Activation recompute (page "Megatron", section "其他关键技术 / 激活重计算":
  * keep fewer forward activations and recompute them in the backward). A
  * caller that keeps only the pre-activation H after tp_mlp_fwd(_ex) rebuilds
@@ -173,6 +238,51 @@ tpmlp_status tp_mlp_recompute_activation(const void* H, void* Y, int64_t n, tpml
 tpmlp_status tp_mlp_recompute_hidden(const void* X, const void* A, const void* a, void* H, void* Y,
                                      int64_t T, int64_t h, int64_t F, int p, tpmlp_dtype dt,
                                      tpmlp_activation act, void* stream);
+
+/* The block with its pre-activation kept in 8 bits between the forward and
+ * the backward (same section): 33/32 bytes per element of H in place of the
+ * four (H and Y) or two (H alone) that the 16-bit forms keep.
+ * The format: every row of H is cut into blocks of 32 columns (the last one
+ * may be shorter). A block holds one power of two 2^e, the smallest with
+ * e ≥ −127 for which every rint(H/2^e) (ties to even) is within ±127, and
+ * those integers. So an element is off by at most 2^(e−1), i.e. 1/127 of the
+ * block's largest magnitude (outside the range where e = −127).
+ *   C: T rows of 32·⌈F/32⌉ int8, zero behind column F; 16-byte aligned.
+ *   S: ⌈F/32⌉ rows of T bytes, S[block][row] = e + 127.
+ * A block with a NaN, an infinity or a magnitude of 127.5·2^121 or more (it
+ * would round to 2^128) has S = 255, and all of its values read as NaN.
+ *
+ * tp_mlp_fwd_ckpt8: H = X·A + a (never stored, quantised from the fp32
+ * accumulator), Y = act(H), Z = Σ Y_i·B_i + b + R. Arguments as
+ * tp_mlp_fwd_ex, with C and S in place of H, and R: T×h of dtype dt, the
+ * residual added to Z, or NULL (R may be Z itself). Y (T×F) holds the
+ * activation on return; the backward does not need it.
+ *
+ * tp_mlp_bwd_ckpt8: with H̃ the values C and S stand for, dH = (dZ·Bᵀ) ⊙
+ * act′(H̃), Y = act(H̃) (rebuilt, written to Y, T×F), dB = Yᵀ·dZ, dA = Xᵀ·dH,
+ * dX = Σ dH_i·A_iᵀ, da = 1ᵀ·dH, db = 1ᵀ·dZ. R's gradient is dZ itself.
+ * Arguments as tp_mlp_bwd_ex; dA, da, dB and db have the type grad_dt:
+ * TPMLP_FP32, or dt for gradients held in the weights' type. Both calls need
+ * tpmlp_ckpt8_workspace_size() bytes (0 for invalid sizes).
+ *
+ * tpmlp_ckpt8_encode writes C and S of a T×F matrix H of dtype dt (for
+ * other activations a caller keeps); tpmlp_ckpt8_decode writes the values C
+ * and S stand for as dtype dt (exact in either type). */
+size_t tpmlp_ckpt8_workspace_size(int64_t T, int64_t h, int64_t F, int p, tpmlp_dtype dt);
+tpmlp_status tp_mlp_fwd_ckpt8(const void* X, const void* A, const void* a, const void* B,
+                              const void* b, const void* R, void* C, void* S, void* Y, void* Z,
+                              int64_t T, int64_t h, int64_t F, int p, tpmlp_dtype dt,
+                              tpmlp_activation act, void* workspace, size_t workspace_bytes,
+                              void* stream);
+tpmlp_status tp_mlp_bwd_ckpt8(const void* dZ, const void* X, const void* A, const void* B,
+                              const void* C, const void* S, void* dX, void* dA, void* da, void* dB,
+                              void* db, void* dH, void* Y, int64_t T, int64_t h, int64_t F, int p,
+                              tpmlp_dtype dt, tpmlp_dtype grad_dt, tpmlp_activation act,
+                              void* workspace, size_t workspace_bytes, void* stream);
+tpmlp_status tpmlp_ckpt8_encode(const void* H, void* C, void* S, int64_t T, int64_t F, tpmlp_dtype dt,
+                                void* stream);
+tpmlp_status tpmlp_ckpt8_decode(const void* C, const void* S, void* H, int64_t T, int64_t F,
+                                tpmlp_dtype dt, void* stream);
 
 /* Static, NUL-terminated description of a status code. */
 const char* tpmlp_strerror(tpmlp_status s);

@@ -15,7 +15,9 @@ def __getattr__(name):
     # The binding loads libtpmlp.so on first use and raises if it is missing;
     # there is no other implementation behind these names.
     if name in ("forward", "backward", "lib", "workspace_size", "set_split_policy",
-                "last_device_status", "TPMLPError", "launch_count"):
+                "last_device_status", "TPMLPError", "launch_count", "layernorm_forward",
+                "layernorm_backward", "fused_linear_forward", "fused_linear_backward",
+                "forward_ckpt8", "backward_ckpt8", "ckpt8_encode", "ckpt8_decode"):
         from . import binding
         return getattr(binding, name)
     raise AttributeError(name)

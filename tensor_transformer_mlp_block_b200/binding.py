@@ -23,7 +23,10 @@ ACTIVATIONS = {"gelu": 0, "gelu_tanh": 1}
 EXPORTS = (
     "tpmlp_workspace_size", "tp_mlp_fwd", "tp_mlp_bwd", "tp_mlp_fwd_ex", "tp_mlp_bwd_ex",
     "tpmlp_linear_workspace_size", "tp_linear_fwd", "tp_linear_bwd",
-    "tp_mlp_recompute_activation", "tp_mlp_recompute_hidden", "tpmlp_strerror",
+    "tpmlp_linear_ex_workspace_size", "tp_linear_fwd_ex", "tp_linear_bwd_ex",
+    "tpmlp_layernorm_workspace_size", "tp_layernorm_fwd", "tp_layernorm_bwd",
+    "tp_mlp_recompute_activation", "tp_mlp_recompute_hidden", "tpmlp_ckpt8_workspace_size",
+    "tp_mlp_fwd_ckpt8", "tp_mlp_bwd_ckpt8", "tpmlp_ckpt8_encode", "tpmlp_ckpt8_decode", "tpmlp_strerror",
     "tpmlp_last_device_status", "tpmlp_set_split_policy", "tpmlp_get_split_policy",
     "tpmlp_set_launch_overlap", "tpmlp_get_launch_overlap", "tpmlp_set_dynamic_schedule",
     "tpmlp_get_dynamic_schedule",
@@ -47,6 +50,8 @@ class TPMLPError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load libtpmlp.so (once). Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):
@@ -88,6 +93,28 @@ def lib() -> ctypes.CDLL:
             L.tp_mlp_recompute_hidden.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, ctypes.c_int,
                                                   ctypes.c_int, ctypes.c_int, vp]
             L.tp_mlp_recompute_hidden.restype = ctypes.c_int
+            L.tpmlp_linear_ex_workspace_size.argtypes = [i64, i64, i64, ci, ci, ci]
+            L.tpmlp_linear_ex_workspace_size.restype = sz
+            L.tp_linear_fwd_ex.argtypes = [vp] * 6 + [i64, i64, i64, ci, ci, ci, ci, vp, sz, vp]
+            L.tp_linear_fwd_ex.restype = ci
+            L.tp_linear_bwd_ex.argtypes = [vp] * 8 + [i64, i64, i64, ci, ci, ci, ci, ci, vp, sz, vp]
+            L.tp_linear_bwd_ex.restype = ci
+            L.tpmlp_layernorm_workspace_size.argtypes = [i64, i64, ci]
+            L.tpmlp_layernorm_workspace_size.restype = sz
+            L.tp_layernorm_fwd.argtypes = [vp] * 6 + [i64, i64, ctypes.c_float, ci, vp]
+            L.tp_layernorm_fwd.restype = ci
+            L.tp_layernorm_bwd.argtypes = [vp] * 9 + [i64, i64, ci, vp, sz, vp]
+            L.tp_layernorm_bwd.restype = ci
+            L.tpmlp_ckpt8_workspace_size.argtypes = [i64, i64, i64, ci, ci]
+            L.tpmlp_ckpt8_workspace_size.restype = sz
+            L.tp_mlp_fwd_ckpt8.argtypes = [vp] * 10 + [i64, i64, i64, ci, ci, ci, vp, sz, vp]
+            L.tp_mlp_fwd_ckpt8.restype = ci
+            L.tp_mlp_bwd_ckpt8.argtypes = [vp] * 13 + [i64, i64, i64, ci, ci, ci, ci, vp, sz, vp]
+            L.tp_mlp_bwd_ckpt8.restype = ci
+            L.tpmlp_ckpt8_encode.argtypes = [vp] * 3 + [i64, i64, ci, vp]
+            L.tpmlp_ckpt8_encode.restype = ci
+            L.tpmlp_ckpt8_decode.argtypes = [vp] * 3 + [i64, i64, ci, vp]
+            L.tpmlp_ckpt8_decode.restype = ci
             L.tpmlp_strerror.argtypes = [ctypes.c_int]
             L.tpmlp_strerror.restype = ctypes.c_char_p
             L.tpmlp_last_device_status.argtypes = [vp]
@@ -448,6 +475,337 @@ def recompute_activation(H, *, out=None, activation: str = "gelu", stream=None):
                                                  _stream_ptr(H.device, stream)),
                "tp_mlp_recompute_activation")
     return Y
+
+
+# ------------------------------------------------- the pre-norm block's operators
+# Outputs and workspaces that these functions allocate belong to the stream the
+# kernels run on (`stream`, or the device's current one), so that the memory is
+# neither reused early nor still in use by other work.
+
+class _Here:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_HERE = _Here()
+
+
+def _scope(dev, stream):
+    """Context in which the stream, and its device, are current."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)
+    return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
+def _rows(X, name):
+    """(T, columns) of the tensor that sets a call's dtype and device."""
+    if X.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, has shape {tuple(X.shape)}")
+    if not X.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return X.shape
+
+
+def _take(t, name, shape, dtype, dev):
+    """Pointer of an argument (None for None) after checking it."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype is not dtype or t.device != dev or not t.is_contiguous():
+        _need(t, name, shape, dtype, dev)
+    return t.data_ptr()
+
+
+def _give(t, name, shape, dtype, dev):
+    """An output: the caller's, checked, or a new one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(t, name, shape, dtype, dev)
+    return t
+
+
+def _work(n, workspace, dev):
+    """(workspace tensor, its bytes) of at least n bytes."""
+    if workspace is None:
+        return torch.empty(n if n > 0 else 1, dtype=torch.uint8, device=dev), n
+    if not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    if workspace.nbytes < n:
+        raise ValueError(f"workspace has {workspace.nbytes} bytes, needs {n}")
+    return workspace, workspace.nbytes
+
+
+def _grad_code(grad_dtype, dtype):
+    if grad_dtype is torch.float32:
+        return FP32
+    if grad_dtype is torch.bfloat16 and dtype is torch.bfloat16:
+        return BF16
+    raise TypeError(f"grad_dtype must be float32 or the weights' dtype {dtype}, not {grad_dtype}")
+
+
+LINEAR_ACTIVATIONS = {"gelu": 0, "gelu_tanh": 1, "none": 2}
+
+
+def _linear_act_code(activation: str) -> int:
+    try:
+        return LINEAR_ACTIVATIONS[activation]
+    except KeyError:
+        raise ValueError(f"activation must be one of {sorted(LINEAR_ACTIVATIONS)}") from None
+
+
+def layernorm_workspace_size(T: int, h: int, dtype: torch.dtype = torch.bfloat16) -> int:
+    return int(lib().tpmlp_layernorm_workspace_size(T, h, BF16 if dtype == torch.bfloat16 else FP32))
+
+
+def layernorm_forward(X, gamma, beta, *, eps: float = 1e-5, stats: bool = True, out=None, stream=None):
+    """Layer norm of the rows of X (T×h): Y = (X − mean)·rstd ⊙ gamma + beta.
+
+    gamma, beta: h, of X's dtype, or None for ones and zeros. Returns
+    (Y, mean, rstd), with the rows' mean and 1/√(var + eps) in fp32 for the
+    backward, or None for both with stats=False; `out` may supply the three."""
+    T, h = _rows(X, "X")
+    dt, dev = X.dtype, X.device
+    code = _dtype_code(X)
+    px = _take(X, "X", (T, h), dt, dev)
+    pg = _take(gamma, "gamma", (h,), dt, dev)
+    pb = _take(beta, "beta", (h,), dt, dev)
+    with _scope(dev, stream):
+        Y, mean, rstd = (None, None, None) if out is None else out
+        Y = _give(Y, "Y", (T, h), dt, dev)
+        if stats:
+            if mean is None and rstd is None:
+                # one allocation for both rows of statistics
+                mean, rstd = torch.empty((2, T), dtype=torch.float32, device=dev).unbind(0)
+            mean = _give(mean, "mean", (T,), torch.float32, dev)
+            rstd = _give(rstd, "rstd", (T,), torch.float32, dev)
+        else:
+            mean = rstd = None
+        st = lib().tp_layernorm_fwd(px, pg, pb, Y.data_ptr(), _ptr(mean), _ptr(rstd), T, h, eps, code,
+                                    torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, "tp_layernorm_fwd")
+    return Y, mean, rstd
+
+
+def layernorm_backward(dY, X, gamma, mean, rstd, *, residual_grad=None, out=None, workspace=None,
+                       stream=None):
+    """Gradients of layernorm_forward for upstream dY (T×h), with the
+    forward's X, gamma (or None), mean and rstd. residual_grad (T×h or None)
+    is added to dX: the gradient that arrives along the residual path.
+    Returns (dX, dgamma, dbeta), dgamma and dbeta fp32."""
+    T, h = _rows(X, "X")
+    dt, dev = X.dtype, X.device
+    f32 = torch.float32
+    code = _dtype_code(X)
+    if mean is None or rstd is None:
+        raise ValueError("mean and rstd of the forward are needed (stats=True)")
+    py = _take(dY, "dY", (T, h), dt, dev)
+    px = _take(X, "X", (T, h), dt, dev)
+    pg = _take(gamma, "gamma", (h,), dt, dev)
+    pm = _take(mean, "mean", (T,), f32, dev)
+    pr = _take(rstd, "rstd", (T,), f32, dev)
+    pd = _take(residual_grad, "residual_grad", (T, h), dt, dev)
+    with _scope(dev, stream):
+        dX, dgamma, dbeta = (None, None, None) if out is None else out
+        dX = _give(dX, "dX", (T, h), dt, dev)
+        if dgamma is None and dbeta is None:
+            dgamma, dbeta = torch.empty((2, h), dtype=f32, device=dev).unbind(0)
+        dgamma = _give(dgamma, "dgamma", (h,), f32, dev)
+        dbeta = _give(dbeta, "dbeta", (h,), f32, dev)
+        L = lib()
+        ws, nb = _work(int(L.tpmlp_layernorm_workspace_size(T, h, code)), workspace, dev)
+        st = L.tp_layernorm_bwd(py, px, pg, pm, pr, pd, dX.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(),
+                                T, h, code, ws.data_ptr(), nb, torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, "tp_layernorm_bwd")
+    return dX, dgamma, dbeta
+
+
+def linear_ex_workspace_size(T: int, K: int, N: int, p: int = 1, split: str = "columns",
+                             dtype: torch.dtype = torch.bfloat16) -> int:
+    code = BF16 if dtype == torch.bfloat16 else FP32
+    return int(lib().tpmlp_linear_ex_workspace_size(T, K, N, p, _split_code(split), code))
+
+
+def fused_linear_forward(X, W, bias, p: int = 1, split: str = "columns", *, activation: str = "none",
+                         residual=None, keep_hidden: bool = False, out=None, hidden=None, workspace=None,
+                         stream=None):
+    """Y = act(X·W + bias) + residual in one product, W split into p shards
+    by "columns" or "rows" (as linear_forward).
+
+    X: T×K, W: K×N, bias: N or None, residual: T×N or None; activation:
+    "none", "gelu" or "gelu_tanh". `out` may supply Y, and may be `residual`
+    (updated in place). With keep_hidden (or a `hidden` tensor) the
+    pre-activation H = X·W + bias is returned too, as (Y, H), for
+    fused_linear_backward."""
+    T, K = _rows(X, "X")
+    N = W.shape[-1]
+    dt, dev = X.dtype, X.device
+    code, split_code, act = _dtype_code(X), _split_code(split), _linear_act_code(activation)
+    if activation == "none" and (keep_hidden or hidden is not None):
+        raise ValueError("without an activation there is no pre-activation to keep")
+    px = _take(X, "X", (T, K), dt, dev)
+    pw = _take(W, "W", (K, N), dt, dev)
+    pb = _take(bias, "bias", (N,), dt, dev)
+    pr = _take(residual, "residual", (T, N), dt, dev)
+    with _scope(dev, stream):
+        Y = _give(out, "out", (T, N), dt, dev)
+        H = _give(hidden, "hidden", (T, N), dt, dev) if keep_hidden or hidden is not None else None
+        L = lib()
+        ws, nb = _work(int(L.tpmlp_linear_ex_workspace_size(T, K, N, int(p), split_code, code)), workspace, dev)
+        st = L.tp_linear_fwd_ex(px, pw, pb, pr, _ptr(H), Y.data_ptr(), T, K, N, int(p), split_code, code, act,
+                                ws.data_ptr(), nb, torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, "tp_linear_fwd_ex")
+    return Y if H is None else (Y, H)
+
+
+def fused_linear_backward(dY, X, W, H=None, p: int = 1, split: str = "columns", *, activation: str = "none",
+                          grad_dtype=torch.float32, out=None, workspace=None, stream=None):
+    """(dX, dW, dbias) of fused_linear_forward for upstream dY (T×N); the
+    residual's gradient is dY itself. H is the forward's pre-activation
+    (None without an activation). dW and dbias have grad_dtype: float32, or
+    the weights' dtype. `out` may supply (dX, dW, dbias) or, with dH (T×N),
+    the scratch gradient of H, (dX, dW, dbias, dH)."""
+    T, K = _rows(X, "X")
+    N = W.shape[-1]
+    dt, dev = X.dtype, X.device
+    code, split_code, act = _dtype_code(X), _split_code(split), _linear_act_code(activation)
+    gcode = _grad_code(grad_dtype, dt)
+    if (activation == "none") != (H is None):
+        raise ValueError("H is the pre-activation that fused_linear_forward kept: needed with an activation, "
+                         "None without")
+    py = _take(dY, "dY", (T, N), dt, dev)
+    px = _take(X, "X", (T, K), dt, dev)
+    pw = _take(W, "W", (K, N), dt, dev)
+    ph = _take(H, "H", (T, N), dt, dev)
+    with _scope(dev, stream):
+        dX, dW, db, dH = (tuple(out or ()) + (None,) * 4)[:4]
+        dX = _give(dX, "dX", (T, K), dt, dev)
+        dW = _give(dW, "dW", (K, N), grad_dtype, dev)
+        db = _give(db, "dbias", (N,), grad_dtype, dev)
+        dH = None if H is None else _give(dH, "dH", (T, N), dt, dev)
+        L = lib()
+        ws, nb = _work(int(L.tpmlp_linear_ex_workspace_size(T, K, N, int(p), split_code, code)), workspace, dev)
+        st = L.tp_linear_bwd_ex(py, px, pw, ph, dX.data_ptr(), dW.data_ptr(), db.data_ptr(), _ptr(dH), T, K, N,
+                                int(p), split_code, code, gcode, act, ws.data_ptr(), nb,
+                                torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, "tp_linear_bwd_ex")
+    return dX, dW, db
+
+
+CKPT8_BLOCK = 32  # columns that share a scale in the 8-bit checkpoint
+
+
+def ckpt8_shapes(T: int, F: int):
+    """Shapes of the 8-bit checkpoint of a T×F matrix: C (int8) and S (uint8)."""
+    blocks = -(-F // CKPT8_BLOCK)
+    return (T, blocks * CKPT8_BLOCK), (blocks, T)
+
+
+def ckpt8_encode(H, *, out=None, stream=None):
+    """The 8-bit copy (C, S) of H (T×F): blocks of 32 columns of a row, a
+    power of two 2^(S − 127) per block and int8 C; `out` may supply both."""
+    T, F = _rows(H, "H")
+    dt, dev = H.dtype, H.device
+    code = _dtype_code(H)
+    ph = _take(H, "H", (T, F), dt, dev)
+    sc, ss = ckpt8_shapes(T, F)
+    with _scope(dev, stream):
+        C, S = (None, None) if out is None else out
+        C = _give(C, "C", sc, torch.int8, dev)
+        S = _give(S, "S", ss, torch.uint8, dev)
+        st = lib().tpmlp_ckpt8_encode(ph, C.data_ptr(), S.data_ptr(), T, F, code,
+                                      torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, "tpmlp_ckpt8_encode")
+    return C, S
+
+
+def ckpt8_decode(C, S, F: int, *, dtype=torch.bfloat16, out=None, stream=None):
+    """The T×F values that C and S stand for (exact in bf16 and fp32)."""
+    T, _ = _rows(C, "C")
+    dev = C.device
+    sc, ss = ckpt8_shapes(T, F)
+    pc = _take(C, "C", sc, torch.int8, dev)
+    ps = _take(S, "S", ss, torch.uint8, dev)
+    with _scope(dev, stream):
+        H = _give(out, "out", (T, F), dtype if out is None else out.dtype, dev)
+        st = lib().tpmlp_ckpt8_decode(pc, ps, H.data_ptr(), T, F, _dtype_code(H),
+                                      torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, "tpmlp_ckpt8_decode")
+    return H
+
+
+def ckpt8_workspace_size(T: int, h: int, F: int, p: int, dtype: torch.dtype = torch.bfloat16) -> int:
+    return int(lib().tpmlp_ckpt8_workspace_size(T, h, F, p, BF16 if dtype == torch.bfloat16 else FP32))
+
+
+def forward_ckpt8(X, A, a, B, b, p: int, *, residual=None, activation: str = "gelu", out=None, scratch=None,
+                  workspace=None, stream=None):
+    """forward() that keeps the pre-activation in 8 bits: Z = act(H)·B + b +
+    residual with H = X·A + a, returning (C, S, Z), C and S the 8-bit copy of
+    H (ckpt8_encode's format) for backward_ckpt8. residual: T×h or None; `out`
+    may supply (C, S, Z), and Z may be `residual` itself. scratch: T×F of X's
+    dtype that holds act(H) on return (allocated if None)."""
+    T, h = _rows(X, "X")
+    F = A.shape[-1]
+    dt, dev = X.dtype, X.device
+    code, act = _dtype_code(X), _act_code(activation)
+    px = _take(X, "X", (T, h), dt, dev)
+    pA = _take(A, "A", (h, F), dt, dev)
+    pa = _take(a, "a", (F,), dt, dev)
+    pB = _take(B, "B", (F, h), dt, dev)
+    pb = _take(b, "b", (h,), dt, dev)
+    pr = _take(residual, "residual", (T, h), dt, dev)
+    sc, ss = ckpt8_shapes(T, F)
+    with _scope(dev, stream):
+        C, S, Z = (None, None, None) if out is None else out
+        C = _give(C, "C", sc, torch.int8, dev)
+        S = _give(S, "S", ss, torch.uint8, dev)
+        Z = _give(Z, "Z", (T, h), dt, dev)
+        Y = _give(scratch, "scratch", (T, F), dt, dev)
+        L = lib()
+        ws, nb = _work(int(L.tpmlp_ckpt8_workspace_size(T, h, F, int(p), code)), workspace, dev)
+        st = L.tp_mlp_fwd_ckpt8(px, pA, pa, pB, pb, pr, C.data_ptr(), S.data_ptr(), Y.data_ptr(), Z.data_ptr(),
+                                T, h, F, int(p), code, act, ws.data_ptr(), nb,
+                                torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, "tp_mlp_fwd_ckpt8")
+    return C, S, Z
+
+
+def backward_ckpt8(dZ, X, A, B, C, S, p: int, *, activation: str = "gelu", grad_dtype=torch.float32, out=None,
+                   workspace=None, stream=None):
+    """backward() from the 8-bit copy of H that forward_ckpt8 left: dH =
+    (dZ·Bᵀ) ⊙ act′(H̃) and Y = act(H̃) with H̃ the values C and S stand for.
+    Returns a dict: dX (T×h), dA (h×F), da (F), dB (F×h), db (h), dH and Y
+    (T×F); dA, da, dB and db have grad_dtype: float32, or the weights' dtype.
+    The residual's gradient is dZ itself. `out` may supply the dict."""
+    T, h = _rows(X, "X")
+    F = A.shape[-1]
+    dt, dev = X.dtype, X.device
+    code, act, gcode = _dtype_code(X), _act_code(activation), _grad_code(grad_dtype, dt)
+    sc, ss = ckpt8_shapes(T, F)
+    pz = _take(dZ, "dZ", (T, h), dt, dev)
+    px = _take(X, "X", (T, h), dt, dev)
+    pA = _take(A, "A", (h, F), dt, dev)
+    pB = _take(B, "B", (F, h), dt, dev)
+    pc = _take(C, "C", sc, torch.int8, dev)
+    ps = _take(S, "S", ss, torch.uint8, dev)
+    with _scope(dev, stream):
+        given = out or {}
+        res = {name: _give(given.get(name), name, shp, d, dev)
+               for name, shp, d in (("dX", (T, h), dt), ("dA", (h, F), grad_dtype), ("da", (F,), grad_dtype),
+                                    ("dB", (F, h), grad_dtype), ("db", (h,), grad_dtype), ("dH", (T, F), dt),
+                                    ("Y", (T, F), dt))}
+        L = lib()
+        ws, nb = _work(int(L.tpmlp_ckpt8_workspace_size(T, h, F, int(p), code)), workspace, dev)
+        st = L.tp_mlp_bwd_ckpt8(pz, px, pA, pB, pc, ps, res["dX"].data_ptr(), res["dA"].data_ptr(),
+                                res["da"].data_ptr(), res["dB"].data_ptr(), res["db"].data_ptr(),
+                                res["dH"].data_ptr(), res["Y"].data_ptr(), T, h, F, int(p), code, gcode, act,
+                                ws.data_ptr(), nb, torch.cuda.current_stream(dev).cuda_stream)
+    _check(st, "tp_mlp_bwd_ckpt8")
+    return res
 
 
 # Work-unit schedules of the tensor-core products (tpmlp_schedule_units).

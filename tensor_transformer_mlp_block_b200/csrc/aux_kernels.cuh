@@ -130,8 +130,12 @@ __global__ void __launch_bounds__(256) colsum_partial2_kernel(const T* __restric
 // contiguous chunk groups; each thread adds its group's chunks in ascending
 // order, then the 8 group sums are added in ascending group order. Fixed
 // assignment and order: bit-reproducible.
+__device__ __forceinline__ void store_f32(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_f32(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
+template <typename O>
 __device__ __forceinline__ void colsum_final_block(const float* __restrict__ partial, int chunks,
-                                                   int64_t C, float* __restrict__ out, int64_t bx) {
+                                                   int64_t C, O* __restrict__ out, int64_t bx) {
     __shared__ float grp[8][32];
     const int64_t c = bx * 32 + threadIdx.x;
     const int per = (chunks + 7) / 8;
@@ -155,14 +159,15 @@ __device__ __forceinline__ void colsum_final_block(const float* __restrict__ par
         float t = grp[0][threadIdx.x];
 #pragma unroll
         for (int y = 1; y < 8; ++y) t += grp[y][threadIdx.x];
-        out[c] = t;
+        store_f32(out + c, t);
     }
 }
 
-// Pass 2 of one matrix: grid ⌈C/32⌉.
+// Pass 2 of one matrix: grid ⌈C/32⌉. O: type of the sums written (rounded once).
+template <typename O>
 __global__ void __launch_bounds__(256) colsum_final_kernel(const float* __restrict__ partial,
                                                           int chunks, int64_t C,
-                                                          float* __restrict__ out) {
+                                                          O* __restrict__ out) {
     grid_dep_wait();  // every input may come from the predecessor kernel
     grid_dep_launch();
     colsum_final_block(partial, chunks, C, out, blockIdx.x);
@@ -171,12 +176,13 @@ __global__ void __launch_bounds__(256) colsum_final_kernel(const float* __restri
 // Pass 2 of two matrices (the column blocks of the first, then of the
 // second: grid ⌈C1/32⌉ + ⌈C2/32⌉); each sum is the one colsum_final_kernel
 // computes.
+template <typename O>
 __global__ void __launch_bounds__(256) colsum_final2_kernel(const float* __restrict__ partial1,
                                                            int chunks1, int64_t C1,
-                                                           float* __restrict__ out1,
+                                                           O* __restrict__ out1,
                                                            const float* __restrict__ partial2,
                                                            int chunks2, int64_t C2,
-                                                           float* __restrict__ out2) {
+                                                           O* __restrict__ out2) {
     grid_dep_wait();
     grid_dep_launch();
     const int64_t nb1 = (C1 + 31) / 32;

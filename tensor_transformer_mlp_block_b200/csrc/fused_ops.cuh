@@ -1,0 +1,723 @@
+// Host side of the layer norm, of the linear layer with bias, activation and
+// residual, and of the block with its pre-activation in 8 bits: argument
+// checks, planning, launches. Part of tpmlp.cu's translation unit (included
+// there), whose helpers it uses.
+
+namespace tpmlp {
+namespace {
+
+using bf16 = __nv_bfloat16;
+
+constexpr int64_t kMaxGridY = 65535;
+
+tpmlp_status check_device() {
+    const DeviceInfo* d = device_info();
+    if (d == nullptr) return TPMLP_ERR_CUDA;
+    return d->cc_major == 10 ? TPMLP_OK : TPMLP_ERR_UNSUPPORTED;
+}
+
+bool known_dtype(tpmlp_dtype dt) { return dt == TPMLP_BF16 || dt == TPMLP_FP32; }
+bool known_act(tpmlp_activation a) { return a == TPMLP_GELU_ERF || a == TPMLP_GELU_TANH; }
+bool known_grad(tpmlp_dtype g, tpmlp_dtype dt) { return g == TPMLP_FP32 || (g == TPMLP_BF16 && dt == TPMLP_BF16); }
+bool fits32(int64_t x) { return x < (int64_t(1) << 31); }
+
+// ------------------------------------------------------------- plain products
+
+// Tiles of simt_tiled_kernel: 128 × 128 (8 × 8 outputs a thread) where that
+// still leaves two tiles per SM, else 64 × 64.
+template <typename TI, typename TO, int EPI>
+tpmlp_status gemm_plain(int kind, const SimtArgs& a, const TI* resid, cudaStream_t st) {
+    const double flops = 2.0 * a.M * a.N * a.K;
+    const double bytes = sizeof(TI) * (1.0 * a.M * a.K + 1.0 * a.K * a.N) + 1.0 * sizeof(TO) * a.M * a.N;
+    const int64_t tiles128 = ((int64_t(a.M) + 127) / 128) * ((int64_t(a.N) + 127) / 128);
+    const int bt = tiles128 >= 2 * plan_num_sms() ? 128 : 64;
+    const int64_t gx = (int64_t(a.M) + bt - 1) / bt, gy = (int64_t(a.N) + bt - 1) / bt;
+    if (gy > kMaxGridY) return TPMLP_ERR_UNSUPPORTED;
+    return timed(kind, flops, bytes, st, [&] {
+        const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
+        if (bt == 128)
+            simt_tiled_kernel<TI, TO, EPI, 128><<<grid, 256, 0, st>>>(a, resid);
+        else
+            simt_tiled_kernel<TI, TO, EPI, 64><<<grid, 256, 0, st>>>(a, resid);
+        return check_launch();
+    });
+}
+
+// Column-tile limits of the plain products and the element-wise kernels (grid
+// y), checked before a call's first launch.
+bool plain_grid_ok(int64_t n) { return (n + 63) / 64 <= kMaxGridY; }
+
+// Aop(m, k), Bop(k, n) of one product by strides.
+SimtArgs plain_args(int64_t M, int64_t N, int64_t K, const void* A, int64_t sam, int64_t sak, const void* B,
+                    int64_t sbk, int64_t sbn, void* out) {
+    SimtArgs a{};
+    a.M = static_cast<int>(M);
+    a.N = static_cast<int>(N);
+    a.K = static_cast<int>(K);
+    a.A = A;
+    a.sam = sam;
+    a.sak = sak;
+    a.B = B;
+    a.sbk = sbk;
+    a.sbn = sbn;
+    a.out0 = out;
+    a.ld_out = N;
+    return a;
+}
+
+// ------------------------------------------------------------------ layer norm
+
+// Shape of a norm kernel's blocks: VE elements per access, `elems` elements
+// per thread, `threads` per row, `rows` rows per block. threads = 0: the row
+// does not fit the registers (looped kernels).
+struct NormShape {
+    int ve, elems, threads, rows;
+};
+
+constexpr int kNormRows = 4;  // rows per block with one warp per row
+
+NormShape norm_shape(int64_t h, int esize, bool vec, bool back) {
+    const int ve = vec ? 16 / esize : 1;
+    const int64_t nvec = h / ve;
+    if (h <= 1024) {  // one warp per row
+        for (int e : {8, 16, 32})
+            if (h <= 32 * e) return {ve, e, 32, kNormRows};
+    }
+    const int limit[3] = {256, 512, back ? 512 : 1024};
+    const int el[3] = {8, 16, 32};
+    for (int i = 0; i < 3; ++i) {
+        const int nv = el[i] / ve;
+        const int64_t t = ((nvec + nv - 1) / nv + 31) / 32 * 32;
+        if (t <= limit[i]) return {ve, el[i], static_cast<int>(t), 1};
+    }
+    return {1, 0, 0, 1};
+}
+
+// Blocks of the backward kernel (each leaves one partial row of dgamma and
+// dbeta): about 1024 threads per SM.
+int64_t norm_bwd_blocks(int64_t T, const NormShape& s) {
+    if (s.threads == 0) return std::min<int64_t>((T + 127) / 128, 1024);
+    const int64_t per_sm = std::max(1, 1024 / (s.threads * s.rows));
+    return std::max<int64_t>(1, std::min((T + s.rows - 1) / s.rows, plan_num_sms() * per_sm));
+}
+
+size_t norm_workspace(int64_t T, int64_t h, tpmlp_dtype dt) {
+    const int esize = dt == TPMLP_BF16 ? 2 : 4;
+    int64_t blocks = norm_bwd_blocks(T, norm_shape(h, esize, false, true));
+    if (h % (16 / esize) == 0) blocks = std::max(blocks, norm_bwd_blocks(T, norm_shape(h, esize, true, true)));
+    return 2 * round256(static_cast<size_t>(blocks) * h * sizeof(float));
+}
+
+template <typename T, int VE, int NV>
+tpmlp_status norm_fwd_launch(const NormShape& s, const T* X, const T* gamma, const T* beta, T* Y, float* mean,
+                             float* rstd, int64_t R, int64_t h, float eps, cudaStream_t st) {
+    const dim3 grid(static_cast<unsigned>((R + s.rows - 1) / s.rows)), block(s.threads, s.rows);
+    return launch_dep(norm_fwd_kernel<T, VE, NV>, grid, block, 0, st, X, gamma, beta, Y, mean, rstd, R,
+                      static_cast<int>(h), eps);
+}
+
+template <typename T, int VE, int NV>
+tpmlp_status norm_bwd_launch(const NormShape& s, const T* dY, const T* X, const T* gamma, const float* mean,
+                             const float* rstd, const T* dR, T* dX, float* pg, float* pb, int64_t blocks,
+                             int64_t R, int64_t h, cudaStream_t st) {
+    const size_t fold = s.rows > 1 ? static_cast<size_t>(s.rows) * h * sizeof(float) : 0;
+    return launch_dep(norm_bwd_kernel<T, VE, NV>, dim3(static_cast<unsigned>(blocks)), dim3(s.threads, s.rows),
+                      fold, st, dY, X, gamma, mean, rstd, dR, dX, pg, pb, R, static_cast<int>(h));
+}
+
+// Calls f.template operator()<VE, NV>() for the shape's vector width and count.
+template <typename T, class F>
+tpmlp_status norm_dispatch(const NormShape& s, F&& f) {
+    constexpr int kVec = 16 / sizeof(T);
+    if (s.ve == 1) {
+        switch (s.elems) {
+            case 8: return f.template operator()<1, 8>();
+            case 16: return f.template operator()<1, 16>();
+            default: return f.template operator()<1, 32>();
+        }
+    }
+    switch (s.elems) {
+        case 8: return f.template operator()<kVec, 8 / kVec>();
+        case 16: return f.template operator()<kVec, 16 / kVec>();
+        default: return f.template operator()<kVec, 32 / kVec>();
+    }
+}
+
+template <typename T>
+struct NormFwdCall {
+    NormShape s;
+    const T *X, *gamma, *beta;
+    T* Y;
+    float *mean, *rstd;
+    int64_t R, h;
+    float eps;
+    cudaStream_t st;
+    template <int VE, int NV>
+    tpmlp_status operator()() const {
+        return norm_fwd_launch<T, VE, NV>(s, X, gamma, beta, Y, mean, rstd, R, h, eps, st);
+    }
+};
+
+template <typename T>
+struct NormBwdCall {
+    NormShape s;
+    const T *dY, *X, *gamma;
+    const float *mean, *rstd;
+    const T* dR;
+    T* dX;
+    float *pg, *pb;
+    int64_t blocks, R, h;
+    cudaStream_t st;
+    template <int VE, int NV>
+    tpmlp_status operator()() const {
+        return norm_bwd_launch<T, VE, NV>(s, dY, X, gamma, mean, rstd, dR, dX, pg, pb, blocks, R, h, st);
+    }
+};
+
+template <typename T>
+tpmlp_status norm_fwd_impl(const void* X, const void* gamma, const void* beta, void* Y, float* mean,
+                           float* rstd, int64_t R, int64_t h, float eps, cudaStream_t st) {
+    const bool vec = h % (16 / sizeof(T)) == 0 && aligned16(X) && aligned16(Y) && aligned16(gamma) &&
+                     aligned16(beta);
+    const NormShape s = norm_shape(h, sizeof(T), vec, false);
+    const double bytes = sizeof(T) * (2.0 * R * h + 2.0 * h) + 8.0 * R;
+    return timed(K_N_FWD, 0.0, bytes, st, [&] {
+        if (s.threads == 0)
+            return launch_dep(norm_fwd_wide_kernel<T>, dim3(static_cast<unsigned>(R)), dim3(1024), 0, st,
+                              static_cast<const T*>(X), static_cast<const T*>(gamma),
+                              static_cast<const T*>(beta), static_cast<T*>(Y), mean, rstd, h, eps);
+        return norm_dispatch<T>(s, NormFwdCall<T>{s, static_cast<const T*>(X), static_cast<const T*>(gamma),
+                                                  static_cast<const T*>(beta), static_cast<T*>(Y), mean, rstd,
+                                                  R, h, eps, st});
+    });
+}
+
+template <typename T>
+tpmlp_status norm_bwd_impl(const void* dY, const void* X, const void* gamma, const float* mean,
+                           const float* rstd, const void* dR, void* dX, float* dgamma, float* dbeta, int64_t R,
+                           int64_t h, void* workspace, cudaStream_t st) {
+    const bool vec = h % (16 / sizeof(T)) == 0 && aligned16(dY) && aligned16(X) && aligned16(gamma) &&
+                     aligned16(dR) && aligned16(dX);
+    const NormShape s = norm_shape(h, sizeof(T), vec, true);
+    const int64_t blocks = norm_bwd_blocks(R, s);
+    float* pg = static_cast<float*>(workspace);
+    float* pb = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                         round256(static_cast<size_t>(blocks) * h * sizeof(float)));
+    const T* y = static_cast<const T*>(dY);
+    const T* x = static_cast<const T*>(X);
+    const T* g = static_cast<const T*>(gamma);
+    const T* d = static_cast<const T*>(dR);
+    T* dx = static_cast<T*>(dX);
+    const double bytes = sizeof(T) * ((dR ? 4.0 : 3.0) * R * h + h) + 8.0 * R + 8.0 * blocks * h;
+    TPMLP_TRY(timed(K_N_BWD, 0.0, bytes, st, [&]() -> tpmlp_status {
+        if (s.threads == 0) {
+            const dim3 cols(static_cast<unsigned>(blocks), static_cast<unsigned>((h + 255) / 256));
+            TPMLP_TRY(launch_dep(norm_bwd_wide_cols_kernel<T>, cols, dim3(256), 0, st, y, x, mean, rstd, pg, pb,
+                                 R, h, (R + blocks - 1) / blocks));
+            return launch_dep(norm_bwd_wide_kernel<T>, dim3(static_cast<unsigned>(R)), dim3(1024), 0, st, y, x,
+                              g, mean, rstd, d, dx, h);
+        }
+        return norm_dispatch<T>(s, NormBwdCall<T>{s, y, x, g, mean, rstd, d, dx, pg, pb, blocks, R, h, st});
+    }));
+    return colsum_finish2(K_N_DGB, pg, blocks, h, dgamma, pb, blocks, h, dbeta, st);
+}
+
+// -------------------------------------------- linear layer, fused epilogue
+
+// The forward's product with EPI (kResid) on the tensor cores.
+template <int EPI>
+tpmlp_status linear_ex_tc(const void* X, const void* W, int T, int N, int K, const SchedReq& req, const GemmArgs& g,
+                          cudaStream_t st) {
+    return gemm_tc<256, false, true, EPI>(K_L_FWD, X, W, T, N, K, req, g, st);
+}
+
+template <typename T, int EPI>
+tpmlp_status linear_ex_plain(const SimtArgs& a, const void* R, cudaStream_t st) {
+    return gemm_plain<T, T, EPI>(K_L_FWD, a, static_cast<const T*>(R), st);
+}
+
+template <typename T>
+tpmlp_status linear_ex_plain_any(tpmlp_activation act, bool keep, const SimtArgs& a, const void* R,
+                                 cudaStream_t st) {
+    if (act == TPMLP_ACT_NONE) return linear_ex_plain<T, EPI_ADD>(a, R, st);
+    if (act == TPMLP_GELU_ERF)
+        return keep ? linear_ex_plain<T, EPI_GELU_ADD>(a, R, st) : linear_ex_plain<T, EPI_ACT_ADD>(a, R, st);
+    return keep ? linear_ex_plain<T, EPI_GELU_ADD_TANH>(a, R, st)
+                : linear_ex_plain<T, EPI_ACT_ADD_TANH>(a, R, st);
+}
+
+tpmlp_status linear_fwd_ex_impl(const void* X, const void* W, const void* bias, const void* R, void* H, void* Y,
+                                int64_t T, int64_t K, int64_t N, int p, int split, tpmlp_dtype dt,
+                                tpmlp_activation act, void* workspace, size_t workspace_bytes,
+                                cudaStream_t st) {
+    LinPlan pl;
+    TPMLP_TRY(lin_checks(T, K, N, p, split, dt, &pl, workspace, workspace_bytes));
+    if (act != TPMLP_ACT_NONE && !known_act(act)) return TPMLP_ERR_INVALID;
+    if (act == TPMLP_ACT_NONE && H != nullptr) return TPMLP_ERR_INVALID;
+    if (T == 0) return TPMLP_OK;
+    if (!X || !W || !Y) return TPMLP_ERR_INVALID;
+    const int iT = static_cast<int>(T), iK = static_cast<int>(K), iN = static_cast<int>(N);
+    if (pl.tc) {
+        for (const void* q : {X, W, bias, R, static_cast<const void*>(H), static_cast<const void*>(Y)})
+            if (q && !aligned16(q)) return TPMLP_ERR_ALIGN;
+        // the relaying activation epilogues run whole tiles (kSplittable)
+        const SchedReq req = (act != TPMLP_ACT_NONE && K >= kRelayMinKAct) ? SchedReq{} : pl.fwd;
+        GemmArgs g{};
+        set_split_space(g, workspace, pl.off_part, pl.off_ctr);
+        if (req.kind != SCHED_TILES) TPMLP_TRY(reset_counters(workspace, pl.off_ctr, pl.ctr_bytes, st));
+        g.out0 = H != nullptr ? H : Y;
+        g.out1 = Y;
+        g.ld_out = N;
+        g.bias = static_cast<const bf16*>(bias);
+        g.resid = static_cast<const bf16*>(R);
+        if (act == TPMLP_ACT_NONE)
+            return R ? linear_ex_tc<EPI_ADD>(X, W, iT, iN, iK, req, g, st)
+                     : linear_ex_tc<EPI_BIAS>(X, W, iT, iN, iK, req, g, st);
+        if (act == TPMLP_GELU_ERF) {
+            if (!H) return linear_ex_tc<EPI_ACT_ADD>(X, W, iT, iN, iK, req, g, st);
+            return R ? linear_ex_tc<EPI_GELU_ADD>(X, W, iT, iN, iK, req, g, st)
+                     : linear_ex_tc<EPI_GELU>(X, W, iT, iN, iK, req, g, st);
+        }
+        if (!H) return linear_ex_tc<EPI_ACT_ADD_TANH>(X, W, iT, iN, iK, req, g, st);
+        return R ? linear_ex_tc<EPI_GELU_ADD_TANH>(X, W, iT, iN, iK, req, g, st)
+                 : linear_ex_tc<EPI_GELU_TANH>(X, W, iT, iN, iK, req, g, st);
+    }
+    if (!plain_grid_ok(N)) return TPMLP_ERR_UNSUPPORTED;
+    SimtArgs a = plain_args(T, N, K, X, K, 1, W, N, 1, H != nullptr ? H : Y);
+    a.out1 = Y;
+    a.bias = bias;
+    if (dt == TPMLP_FP32) return linear_ex_plain_any<float>(act, H != nullptr, a, R, st);
+    return linear_ex_plain_any<bf16>(act, H != nullptr, a, R, st);
+}
+
+template <typename T, bool TANH>
+tpmlp_status act_grad_launch(const void* dY, const void* H, void* dH, int64_t R, int64_t C, int64_t chunks,
+                             float* partial, cudaStream_t st) {
+    const dim3 grid(static_cast<unsigned>(chunks), static_cast<unsigned>((C + 255) / 256));
+    const T *y = static_cast<const T*>(dY), *x = static_cast<const T*>(H);
+    if (C % 8 == 0 && aligned16(dY) && aligned16(H) && aligned16(dH))
+        return launch_dep(act_grad_kernel<T, TANH, true>, grid, dim3(32, 8), 0, st, y, x, static_cast<T*>(dH), R,
+                          C, kColsumRowsPerChunk, partial);
+    return launch_dep(act_grad_kernel<T, TANH, false>, grid, dim3(32, 8), 0, st, y, x, static_cast<T*>(dH), R, C,
+                      kColsumRowsPerChunk, partial);
+}
+
+// TG: type of dW and dbias. T: type of the rest.
+template <typename T, typename TG>
+tpmlp_status linear_bwd_ex_run(const LinPlan& pl, const void* dY, const void* X, const void* W, const void* H,
+                               void* dX, void* dW, void* dbias, void* dH, int64_t R, int64_t K, int64_t N,
+                               tpmlp_activation act, void* workspace, cudaStream_t st) {
+    float* cs = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.off_cs);
+    TG* db = static_cast<TG*>(dbias);
+    const void* g = dY;
+    if (act == TPMLP_ACT_NONE) {
+        TPMLP_TRY(colsum(K_L_DB, static_cast<const T*>(dY), R, N, pl.chunks, cs, db, st));
+    } else {
+        g = dH;
+        TPMLP_TRY(timed(K_L_DH, 0.0, 3.0 * sizeof(T) * double(R) * N, st, [&] {
+            return act == TPMLP_GELU_TANH ? act_grad_launch<T, true>(dY, H, dH, R, N, pl.chunks, cs, st)
+                                          : act_grad_launch<T, false>(dY, H, dH, R, N, pl.chunks, cs, st);
+        }));
+        TPMLP_TRY(timed(K_L_DB, 0.0, 4.0 * (double(pl.chunks) + 1) * N, st, [&] {
+            return launch_dep(colsum_final_kernel<TG>, dim3(static_cast<unsigned>((N + 31) / 32)), dim3(32, 8), 0,
+                              st, static_cast<const float*>(cs), static_cast<int>(pl.chunks), N, db);
+        }));
+    }
+    if constexpr (sizeof(T) == 2) {
+        if (pl.tc) {
+            const int iT = static_cast<int>(R), iK = static_cast<int>(K), iN = static_cast<int>(N);
+            GemmArgs gw{};
+            set_split_space(gw, workspace, pl.off_part, pl.off_ctr);
+            if (pl.bwd_split)
+                TPMLP_TRY(zero_counters_before(gw, pl.dw, workspace, pl.off_ctr, pl.ctr_bytes, st));
+            gw.out0 = dW;
+            gw.ld_out = N;
+            TPMLP_TRY((gemm_tc<256, true, true, sizeof(TG) == 2 ? EPI_BIAS : EPI_F32>(K_L_DW, X, g, iK, iN, iT, pl.dw,
+                                                                                     gw, st)));
+            GemmArgs gx{};
+            set_split_space(gx, workspace, pl.off_part, pl.off_ctr);
+            gx.out0 = dX;
+            gx.ld_out = K;
+            return gemm_tc<256, false, false, EPI_BIAS>(K_L_DX, g, W, iT, iK, iN, pl.dx, gx, st);
+        }
+    }
+    TPMLP_TRY((gemm_plain<T, TG, EPI_F32>(K_L_DW, plain_args(K, N, R, X, 1, K, g, N, 1, dW), nullptr, st)));
+    return gemm_plain<T, T, EPI_F32>(K_L_DX, plain_args(R, K, N, g, N, 1, W, 1, N, dX), nullptr, st);
+}
+
+// ------------------------------------------------------------ 8-bit checkpoint
+
+int64_t c8_blocks(int64_t F) { return (F + kC8Block - 1) / kC8Block; }
+
+template <typename TI, typename T, int ACT>
+tpmlp_status ckpt8_encode_launch(const void* H, const void* bias, void* Y, void* C, void* S, int64_t R, int64_t F,
+                                 cudaStream_t st) {
+    const dim3 grid(static_cast<unsigned>((R + 31) / 32), static_cast<unsigned>((F + 255) / 256));
+    const bool vec = F % 8 == 0 && aligned16(H) && aligned16(Y);
+    auto kern = vec ? ckpt8_encode_kernel<TI, T, ACT, true> : ckpt8_encode_kernel<TI, T, ACT, false>;
+    return launch_dep(kern, grid, dim3(256), 0, st, static_cast<const TI*>(H), static_cast<const T*>(bias),
+                      static_cast<T*>(Y), static_cast<uint8_t*>(C), static_cast<uint8_t*>(S), R, F);
+}
+
+template <typename T, int ACT>
+tpmlp_status ckpt8_decode_launch(const void* C, const void* S, const float* P, void* out0, void* out1, int64_t R,
+                                 int64_t F, cudaStream_t st) {
+    const dim3 grid(static_cast<unsigned>((R + 31) / 32), static_cast<unsigned>((F + 255) / 256));
+    const bool vec = F % 8 == 0 && aligned16(P) && aligned16(out0) && aligned16(out1);
+    auto kern = vec ? ckpt8_decode_kernel<T, ACT, true> : ckpt8_decode_kernel<T, ACT, false>;
+    return launch_dep(kern, grid, dim3(256), 0, st, static_cast<const uint8_t*>(C), static_cast<const uint8_t*>(S),
+                      P, static_cast<T*>(out0), static_cast<T*>(out1), R, F);
+}
+
+// The MLP's plan plus, on the plain path, one T × F fp32 product (before the
+// activation is applied and H quantised, or dZ·Bᵀ).
+bool make_c8_plan(int64_t T, int64_t h, int64_t F, int p, tpmlp_dtype dt, Plan* pl, size_t* off_prod,
+                  size_t* total) {
+    if (!make_plan(T, h, F, p, dt, pl)) return false;
+    *off_prod = pl->total;
+    *total = pl->total + (pl->tc ? 0 : round256(static_cast<size_t>(T) * F * sizeof(float)));
+    return true;
+}
+
+tpmlp_status c8_checks(int64_t T, int64_t h, int64_t F, int p, tpmlp_dtype dt, tpmlp_activation act, Plan* pl,
+                       size_t* off_prod, void* ws, size_t ws_bytes) {
+    size_t total = 0;
+    if (!make_c8_plan(T, h, F, p, dt, pl, off_prod, &total) || !known_act(act)) return TPMLP_ERR_INVALID;
+    if (!fits32(T) || !fits32(h) || !fits32(F) || !plain_grid_ok(F) || !plain_grid_ok(h))
+        return TPMLP_ERR_UNSUPPORTED;
+    TPMLP_TRY(check_device());
+    if (total > 0 && (ws == nullptr || ws_bytes < total)) return TPMLP_ERR_WORKSPACE;
+    return ws != nullptr && !aligned16(ws) ? TPMLP_ERR_ALIGN : TPMLP_OK;
+}
+
+template <int EPI>
+tpmlp_status c8_fwd_tc(const Plan& pl, const void* X, const void* A, const void* a, const void* B, const void* b,
+                       const void* R, void* C, void* S, void* Y, void* Z, int64_t T, int64_t h, int64_t F,
+                       void* workspace, cudaStream_t st) {
+    const int iT = static_cast<int>(T), ih = static_cast<int>(h), iF = static_cast<int>(F);
+    GemmArgs g1{};
+    set_split_space(g1, workspace, pl.off_part, pl.off_ctr);
+    g1.dyn_counter = dyn_space(workspace, pl.off_dyn);
+    if (pl.fwd_dyn)
+        TPMLP_TRY(reset_counters(workspace, pl.off_ctr, pl.ctr_bytes, st));
+    else if (pl.fwd_split)
+        TPMLP_TRY(zero_counters_before(g1, pl.f1, workspace, pl.off_ctr, pl.ctr_bytes, st));
+    g1.out0 = Y;
+    g1.ld_out = F;
+    g1.bias = static_cast<const bf16*>(a);
+    g1.c8 = static_cast<uint8_t*>(C);
+    g1.c8_scale = static_cast<uint8_t*>(S);
+    g1.c8_ld = c8_blocks(F) * kC8Block;
+    TPMLP_TRY((gemm_tc<256, false, true, EPI>(K_F1, X, A, iT, iF, ih, pl.f1, g1, st)));
+    GemmArgs g2{};
+    set_split_space(g2, workspace, pl.off_part, pl.off_ctr);
+    g2.dyn_counter = dyn_space(workspace, pl.off_dyn);
+    g2.out0 = Z;
+    g2.ld_out = h;
+    g2.bias = static_cast<const bf16*>(b);
+    g2.resid = static_cast<const bf16*>(R);
+    if (R) return gemm_tc<256, false, true, EPI_ADD>(K_F2, Y, B, iT, ih, iF, pl.f2, g2, st);
+    return gemm_tc<256, false, true, EPI_BIAS>(K_F2, Y, B, iT, ih, iF, pl.f2, g2, st);
+}
+
+template <typename T>
+tpmlp_status c8_fwd_plain(const void* X, const void* A, const void* a, const void* B, const void* b, const void* R,
+                          void* C, void* S, void* Y, void* Z, float* prod, int64_t rows, int64_t h, int64_t F,
+                          tpmlp_activation act, cudaStream_t st) {
+    TPMLP_TRY((gemm_plain<T, float, EPI_F32>(K_F1, plain_args(rows, F, h, X, h, 1, A, F, 1, prod), nullptr, st)));
+    TPMLP_TRY(timed(K_C8, 0.0, (4.0 + 33.0 / 32.0 + sizeof(T)) * rows * F, st, [&] {
+        return act == TPMLP_GELU_TANH ? ckpt8_encode_launch<float, T, 2>(prod, a, Y, C, S, rows, F, st)
+                                      : ckpt8_encode_launch<float, T, 1>(prod, a, Y, C, S, rows, F, st);
+    }));
+    SimtArgs s2 = plain_args(rows, h, F, Y, F, 1, B, h, 1, Z);
+    s2.bias = b;
+    return gemm_plain<T, T, EPI_ADD>(K_F2, s2, static_cast<const T*>(R), st);
+}
+
+template <int EPI, typename TG>
+tpmlp_status c8_bwd_tc(const Plan& pl, const void* dZ, const void* X, const void* A, const void* B, const void* C,
+                       const void* S, void* dX, TG* dA, TG* da, TG* dB, TG* db, void* dH, void* Y, int64_t T,
+                       int64_t h, int64_t F, void* workspace, cudaStream_t st) {
+    constexpr int kGrad = sizeof(TG) == 2 ? EPI_BIAS : EPI_F32;
+    const int iT = static_cast<int>(T), ih = static_cast<int>(h), iF = static_cast<int>(F);
+    const bf16* dZb = static_cast<const bf16*>(dZ);
+    float* cs_h = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.off_cs_h);
+    float* cs_f = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.off_cs_f);
+    int* dyn = dyn_space(workspace, pl.off_dyn);
+    if (pl.bwd_dyn) TPMLP_TRY(reset_counters(workspace, pl.off_ctr, pl.ctr_bytes, st));
+    // column sums as in bwd_impl: da's partials from the relaying epilogue for
+    // long K, else both sums after the product
+    const bool fused_da = h >= kRelayMinKAct;
+    if (fused_da) TPMLP_TRY(colsum_first(K_B1_DB, dZb, T, h, pl.chunks, cs_h, st));
+    GemmArgs g2{};
+    set_split_space(g2, workspace, pl.off_part, pl.off_ctr);
+    g2.dyn_counter = dyn;
+    if (pl.bwd_split && !pl.bwd_dyn)
+        TPMLP_TRY(zero_counters_before(g2, pl.b2, workspace, pl.off_ctr, pl.ctr_bytes, st));
+    g2.out0 = dH;
+    g2.out1 = Y;
+    g2.ld_out = F;
+    g2.c8 = static_cast<uint8_t*>(const_cast<void*>(C));
+    g2.c8_scale = static_cast<uint8_t*>(const_cast<void*>(S));
+    g2.c8_ld = c8_blocks(F) * kC8Block;
+    g2.colsum_out = fused_da ? cs_f : nullptr;
+    TPMLP_TRY((gemm_tc<256, false, false, EPI>(K_B2, dZ, B, iT, iF, ih, pl.b2, g2, st)));
+    if (fused_da)
+        TPMLP_TRY(colsum_finish2(K_B12, cs_h, pl.chunks, h, db, cs_f, da_partial_rows(T), F, da, st));
+    else
+        TPMLP_TRY(colsum2(K_B12, dZb, h, cs_h, db, static_cast<const bf16*>(dH), F, cs_f, da, T, pl.chunks, st));
+    if (pl.group34) {
+        TPMLP_TRY((gemm_tc_grouped<256, true, true, kGrad>(K_B34, Y, dZ, iF, ih, dB, X, dH, ih, iF, dA, iT, st)));
+    } else {
+        GemmArgs g3{};
+        set_split_space(g3, workspace, pl.off_part, pl.off_ctr);
+        g3.out0 = dB;
+        g3.ld_out = h;
+        TPMLP_TRY((gemm_tc<256, true, true, kGrad>(K_B3, Y, dZ, iF, ih, iT, pl.b3, g3, st)));
+        GemmArgs g4{};
+        set_split_space(g4, workspace, pl.off_part, pl.off_ctr);
+        g4.out0 = dA;
+        g4.ld_out = F;
+        TPMLP_TRY((gemm_tc<256, true, true, kGrad>(K_B4, X, dH, ih, iF, iT, pl.b4, g4, st)));
+    }
+    GemmArgs g5{};
+    set_split_space(g5, workspace, pl.off_part, pl.off_ctr);
+    g5.dyn_counter = dyn;
+    g5.out0 = dX;
+    g5.ld_out = h;
+    return gemm_tc<256, false, false, EPI_BIAS>(K_B5, dH, A, iT, ih, iF, pl.b5, g5, st);
+}
+
+template <typename T, typename TG>
+tpmlp_status c8_bwd_plain(const Plan& pl, const void* dZ, const void* X, const void* A, const void* B, const void* C,
+                          const void* S, void* dX, TG* dA, TG* da, TG* dB, TG* db, void* dH, void* Y, float* prod,
+                          int64_t rows, int64_t h, int64_t F, tpmlp_activation act, void* workspace,
+                          cudaStream_t st) {
+    float* cs_h = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.off_cs_h);
+    float* cs_f = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.off_cs_f);
+    TPMLP_TRY((gemm_plain<T, float, EPI_F32>(K_B2, plain_args(rows, F, h, dZ, h, 1, B, 1, h, prod), nullptr, st)));
+    TPMLP_TRY(timed(K_C8, 0.0, (4.0 + 33.0 / 32.0 + 2.0 * sizeof(T)) * rows * F, st, [&] {
+        return act == TPMLP_GELU_TANH ? ckpt8_decode_launch<T, 2>(C, S, prod, dH, Y, rows, F, st)
+                                      : ckpt8_decode_launch<T, 1>(C, S, prod, dH, Y, rows, F, st);
+    }));
+    TPMLP_TRY(colsum2(K_B12, static_cast<const T*>(dZ), h, cs_h, db, static_cast<const T*>(dH), F, cs_f, da, rows,
+                      pl.chunks, st));
+    TPMLP_TRY((gemm_plain<T, TG, EPI_F32>(K_B3, plain_args(F, h, rows, Y, 1, F, dZ, h, 1, dB), nullptr, st)));
+    TPMLP_TRY((gemm_plain<T, TG, EPI_F32>(K_B4, plain_args(h, F, rows, X, 1, h, dH, F, 1, dA), nullptr, st)));
+    return gemm_plain<T, T, EPI_F32>(K_B5, plain_args(rows, h, F, dH, F, 1, A, 1, F, dX), nullptr, st);
+}
+
+template <typename TG>
+tpmlp_status c8_bwd_typed(const Plan& pl, const void* dZ, const void* X, const void* A, const void* B, const void* C,
+                          const void* S, void* dX, void* dA, void* da, void* dB, void* db, void* dH, void* Y,
+                          float* prod, int64_t T, int64_t h, int64_t F, tpmlp_dtype dt, tpmlp_activation act,
+                          void* workspace, cudaStream_t st) {
+    TG *gA = static_cast<TG*>(dA), *ga = static_cast<TG*>(da), *gB = static_cast<TG*>(dB),
+       *gb = static_cast<TG*>(db);
+    if (pl.tc) {
+        if (act == TPMLP_GELU_TANH)
+            return c8_bwd_tc<EPI_DGELU_C8_TANH, TG>(pl, dZ, X, A, B, C, S, dX, gA, ga, gB, gb, dH, Y, T, h, F,
+                                                    workspace, st);
+        return c8_bwd_tc<EPI_DGELU_C8, TG>(pl, dZ, X, A, B, C, S, dX, gA, ga, gB, gb, dH, Y, T, h, F, workspace,
+                                           st);
+    }
+    if constexpr (sizeof(TG) == 4) {
+        if (dt == TPMLP_FP32)
+            return c8_bwd_plain<float, TG>(pl, dZ, X, A, B, C, S, dX, gA, ga, gB, gb, dH, Y, prod, T, h, F, act,
+                                           workspace, st);
+    }
+    return c8_bwd_plain<bf16, TG>(pl, dZ, X, A, B, C, S, dX, gA, ga, gB, gb, dH, Y, prod, T, h, F, act, workspace,
+                                  st);
+}
+
+// n elements of type dt set to zero (an all-zero pattern in either type).
+tpmlp_status zero_any(void* p, int64_t n, tpmlp_dtype dt, cudaStream_t st) {
+    if (dt == TPMLP_FP32) return zero_f32(static_cast<float*>(p), n, st);
+    return cudaMemsetAsync(p, 0, static_cast<size_t>(n) * 2, st) == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace tpmlp
+
+extern "C" {
+
+size_t tpmlp_layernorm_workspace_size(int64_t T, int64_t h, tpmlp_dtype dt) {
+    if (T < 0 || h < 1 || !fits32(T) || !fits32(h) || !known_dtype(dt)) return 0;
+    return norm_workspace(T, h, dt);
+}
+
+tpmlp_status tp_layernorm_fwd(const void* X, const void* gamma, const void* beta, void* Y, float* mean, float* rstd,
+                              int64_t T, int64_t h, float eps, tpmlp_dtype dt, void* stream) {
+    cudaGetLastError();
+    // eps >= 0 and finite; a NaN fails both comparisons
+    if (T < 0 || h < 1 || !known_dtype(dt) || !(eps >= 0.0f && eps <= 3.0e38f)) return TPMLP_ERR_INVALID;
+    if ((mean == nullptr) != (rstd == nullptr)) return TPMLP_ERR_INVALID;
+    if (T > 0 && (!X || !Y)) return TPMLP_ERR_INVALID;
+    if (!fits32(T) || !fits32(h)) return TPMLP_ERR_UNSUPPORTED;
+    TPMLP_TRY(check_device());
+    if (T == 0) return TPMLP_OK;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (dt == TPMLP_BF16) return norm_fwd_impl<bf16>(X, gamma, beta, Y, mean, rstd, T, h, eps, st);
+    return norm_fwd_impl<float>(X, gamma, beta, Y, mean, rstd, T, h, eps, st);
+}
+
+tpmlp_status tp_layernorm_bwd(const void* dY, const void* X, const void* gamma, const float* mean,
+                              const float* rstd, const void* dR, void* dX, float* dgamma, float* dbeta, int64_t T,
+                              int64_t h, tpmlp_dtype dt, void* workspace, size_t workspace_bytes, void* stream) {
+    cudaGetLastError();
+    if (T < 0 || h < 1 || !known_dtype(dt) || !dgamma || !dbeta) return TPMLP_ERR_INVALID;
+    if (T > 0 && (!dY || !X || !mean || !rstd || !dX)) return TPMLP_ERR_INVALID;
+    if (!fits32(T) || !fits32(h) || (h + 255) / 256 > kMaxGridY) return TPMLP_ERR_UNSUPPORTED;
+    TPMLP_TRY(check_device());
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) {
+        TPMLP_TRY(zero_f32(dgamma, h, st));
+        return zero_f32(dbeta, h, st);
+    }
+    if (workspace == nullptr || workspace_bytes < norm_workspace(T, h, dt)) return TPMLP_ERR_WORKSPACE;
+    if (!aligned16(workspace)) return TPMLP_ERR_ALIGN;
+    if (dt == TPMLP_BF16)
+        return norm_bwd_impl<bf16>(dY, X, gamma, mean, rstd, dR, dX, dgamma, dbeta, T, h, workspace, st);
+    return norm_bwd_impl<float>(dY, X, gamma, mean, rstd, dR, dX, dgamma, dbeta, T, h, workspace, st);
+}
+
+size_t tpmlp_linear_ex_workspace_size(int64_t T, int64_t K, int64_t N, int p, tpmlp_split split, tpmlp_dtype dt) {
+    LinPlan pl;
+    if (!make_lin_plan(T, K, N, p, static_cast<int>(split), dt, &pl)) return 0;
+    return pl.total;
+}
+
+tpmlp_status tp_linear_fwd_ex(const void* X, const void* W, const void* bias, const void* R, void* H, void* Y,
+                              int64_t T, int64_t K, int64_t N, int p, tpmlp_split split, tpmlp_dtype dt,
+                              tpmlp_activation act, void* workspace, size_t workspace_bytes, void* stream) {
+    cudaGetLastError();
+    return linear_fwd_ex_impl(X, W, bias, R, H, Y, T, K, N, p, static_cast<int>(split), dt, act, workspace,
+                              workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+tpmlp_status tp_linear_bwd_ex(const void* dY, const void* X, const void* W, const void* H, void* dX, void* dW,
+                              void* dbias, void* dH, int64_t T, int64_t K, int64_t N, int p, tpmlp_split split,
+                              tpmlp_dtype dt, tpmlp_dtype grad_dt, tpmlp_activation act, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+    cudaGetLastError();
+    LinPlan pl;
+    TPMLP_TRY(lin_checks(T, K, N, p, static_cast<int>(split), dt, &pl, workspace, workspace_bytes));
+    if (!known_grad(grad_dt, dt) || (act != TPMLP_ACT_NONE && !known_act(act))) return TPMLP_ERR_INVALID;
+    if (!dW || !dbias) return TPMLP_ERR_INVALID;
+    if (act == TPMLP_ACT_NONE && (H || dH)) return TPMLP_ERR_INVALID;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) {
+        TPMLP_TRY(zero_any(dW, K * N, grad_dt, st));
+        return zero_any(dbias, N, grad_dt, st);
+    }
+    if (!dY || !X || !W || !dX || (act != TPMLP_ACT_NONE && (!H || !dH))) return TPMLP_ERR_INVALID;
+    if (pl.tc) {
+        for (const void* q : {dY, X, W, H, static_cast<const void*>(dX), static_cast<const void*>(dW),
+                              static_cast<const void*>(dbias), static_cast<const void*>(dH)})
+            if (q && !aligned16(q)) return TPMLP_ERR_ALIGN;
+    }
+    if (!plain_grid_ok(N) || !plain_grid_ok(K)) return TPMLP_ERR_UNSUPPORTED;
+    if (dt == TPMLP_FP32)
+        return linear_bwd_ex_run<float, float>(pl, dY, X, W, H, dX, dW, dbias, dH, T, K, N, act, workspace, st);
+    if (grad_dt == TPMLP_BF16)
+        return linear_bwd_ex_run<bf16, bf16>(pl, dY, X, W, H, dX, dW, dbias, dH, T, K, N, act, workspace, st);
+    return linear_bwd_ex_run<bf16, float>(pl, dY, X, W, H, dX, dW, dbias, dH, T, K, N, act, workspace, st);
+}
+
+size_t tpmlp_ckpt8_workspace_size(int64_t T, int64_t h, int64_t F, int p, tpmlp_dtype dt) {
+    Plan pl;
+    size_t off = 0, total = 0;
+    if (!make_c8_plan(T, h, F, p, dt, &pl, &off, &total)) return 0;
+    return total;
+}
+
+tpmlp_status tp_mlp_fwd_ckpt8(const void* X, const void* A, const void* a, const void* B, const void* b,
+                              const void* R, void* C, void* S, void* Y, void* Z, int64_t T, int64_t h, int64_t F,
+                              int p, tpmlp_dtype dt, tpmlp_activation act, void* workspace, size_t workspace_bytes,
+                              void* stream) {
+    cudaGetLastError();
+    Plan pl;
+    size_t off = 0;
+    TPMLP_TRY(c8_checks(T, h, F, p, dt, act, &pl, &off, workspace, workspace_bytes));
+    if (T == 0) return TPMLP_OK;
+    if (!X || !A || !B || !C || !S || !Y || !Z) return TPMLP_ERR_INVALID;
+    if (!aligned16(C)) return TPMLP_ERR_ALIGN;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (pl.tc) {
+        for (const void* q : {X, A, a, B, b, R, static_cast<const void*>(Y), static_cast<const void*>(Z)})
+            if (q && !aligned16(q)) return TPMLP_ERR_ALIGN;
+        if (act == TPMLP_GELU_TANH)
+            return c8_fwd_tc<EPI_GELU_C8_TANH>(pl, X, A, a, B, b, R, C, S, Y, Z, T, h, F, workspace, st);
+        return c8_fwd_tc<EPI_GELU_C8>(pl, X, A, a, B, b, R, C, S, Y, Z, T, h, F, workspace, st);
+    }
+    float* prod = reinterpret_cast<float*>(static_cast<char*>(workspace) + off);
+    if (dt == TPMLP_FP32) return c8_fwd_plain<float>(X, A, a, B, b, R, C, S, Y, Z, prod, T, h, F, act, st);
+    return c8_fwd_plain<bf16>(X, A, a, B, b, R, C, S, Y, Z, prod, T, h, F, act, st);
+}
+
+tpmlp_status tp_mlp_bwd_ckpt8(const void* dZ, const void* X, const void* A, const void* B, const void* C,
+                              const void* S, void* dX, void* dA, void* da, void* dB, void* db, void* dH, void* Y,
+                              int64_t T, int64_t h, int64_t F, int p, tpmlp_dtype dt, tpmlp_dtype grad_dt,
+                              tpmlp_activation act, void* workspace, size_t workspace_bytes, void* stream) {
+    cudaGetLastError();
+    Plan pl;
+    size_t off = 0;
+    TPMLP_TRY(c8_checks(T, h, F, p, dt, act, &pl, &off, workspace, workspace_bytes));
+    if (!known_grad(grad_dt, dt) || !dA || !da || !dB || !db) return TPMLP_ERR_INVALID;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (T == 0) {
+        TPMLP_TRY(zero_any(dA, h * F, grad_dt, st));
+        TPMLP_TRY(zero_any(da, F, grad_dt, st));
+        TPMLP_TRY(zero_any(dB, F * h, grad_dt, st));
+        return zero_any(db, h, grad_dt, st);
+    }
+    if (!dZ || !X || !A || !B || !C || !S || !dX || !dH || !Y) return TPMLP_ERR_INVALID;
+    if (!aligned16(C)) return TPMLP_ERR_ALIGN;
+    if (pl.tc) {
+        for (const void* q : {dZ, X, A, B, static_cast<const void*>(dX), static_cast<const void*>(dA),
+                              static_cast<const void*>(da), static_cast<const void*>(dB),
+                              static_cast<const void*>(db), static_cast<const void*>(dH),
+                              static_cast<const void*>(Y)})
+            if (!aligned16(q)) return TPMLP_ERR_ALIGN;
+    }
+    float* prod = reinterpret_cast<float*>(static_cast<char*>(workspace) + off);
+    if (grad_dt == TPMLP_BF16)
+        return c8_bwd_typed<bf16>(pl, dZ, X, A, B, C, S, dX, dA, da, dB, db, dH, Y, prod, T, h, F, dt, act,
+                                  workspace, st);
+    return c8_bwd_typed<float>(pl, dZ, X, A, B, C, S, dX, dA, da, dB, db, dH, Y, prod, T, h, F, dt, act, workspace,
+                               st);
+}
+
+tpmlp_status tpmlp_ckpt8_encode(const void* H, void* C, void* S, int64_t T, int64_t F, tpmlp_dtype dt,
+                                void* stream) {
+    cudaGetLastError();
+    if (T < 0 || F < 1 || !known_dtype(dt) || (T > 0 && (!H || !C || !S))) return TPMLP_ERR_INVALID;
+    if (!fits32(T) || !fits32(F) || !plain_grid_ok(F)) return TPMLP_ERR_UNSUPPORTED;
+    TPMLP_TRY(check_device());
+    if (T == 0) return TPMLP_OK;
+    if (!aligned16(C)) return TPMLP_ERR_ALIGN;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const double esize = dt == TPMLP_BF16 ? 2.0 : 4.0;
+    return timed(K_C8, 0.0, (esize + 33.0 / 32.0) * T * F, st, [&] {
+        return dt == TPMLP_BF16 ? ckpt8_encode_launch<bf16, bf16, 0>(H, nullptr, nullptr, C, S, T, F, st)
+                                : ckpt8_encode_launch<float, float, 0>(H, nullptr, nullptr, C, S, T, F, st);
+    });
+}
+
+tpmlp_status tpmlp_ckpt8_decode(const void* C, const void* S, void* H, int64_t T, int64_t F, tpmlp_dtype dt,
+                                void* stream) {
+    cudaGetLastError();
+    if (T < 0 || F < 1 || !known_dtype(dt) || (T > 0 && (!H || !C || !S))) return TPMLP_ERR_INVALID;
+    if (!fits32(T) || !fits32(F) || !plain_grid_ok(F)) return TPMLP_ERR_UNSUPPORTED;
+    TPMLP_TRY(check_device());
+    if (T == 0) return TPMLP_OK;
+    if (!aligned16(C)) return TPMLP_ERR_ALIGN;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const double esize = dt == TPMLP_BF16 ? 2.0 : 4.0;
+    return timed(K_C8, 0.0, (esize + 33.0 / 32.0) * T * F, st, [&] {
+        return dt == TPMLP_BF16 ? ckpt8_decode_launch<bf16, 0>(C, S, nullptr, H, nullptr, T, F, st)
+                                : ckpt8_decode_launch<float, 0>(C, S, nullptr, H, nullptr, T, F, st);
+    });
+}
+
+}  // extern "C"

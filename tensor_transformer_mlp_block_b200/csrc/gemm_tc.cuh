@@ -35,6 +35,7 @@
 // and tensor memory is freed before the CTA exits.
 #pragma once
 
+#include "ckpt8.cuh"
 #include "ptx.cuh"
 
 namespace tpmlp {
@@ -46,16 +47,38 @@ enum EpiKind : int {
     EPI_F32 = 3,         // out0 = acc (fp32)
     EPI_GELU_TANH = 4,   // as EPI_GELU with the tanh approximation of GeLU
     EPI_DGELU_TANH = 5,  // as EPI_DGELU with the tanh approximation's derivative
+    // the linear layer's epilogues: bias, activation, residual (resid may be null)
+    EPI_ADD = 6,             // out0 = acc + bias + resid
+    EPI_ACT_ADD = 7,             // out0 = GeLU(acc + bias) + resid
+    EPI_ACT_ADD_TANH = 8,        // the same with the tanh approximation
+    EPI_GELU_ADD = 9,        // out0 = H = acc + bias, out1 = GeLU(H) + resid
+    EPI_GELU_ADD_TANH = 10,
+    // the 8-bit checkpoint (ckpt8.cuh): H in 8 bits between the passes
+    EPI_GELU_C8 = 11,        // c8 = H = acc + bias in 8 bits, out0 = Y = GeLU(H)
+    EPI_GELU_C8_TANH = 12,
+    EPI_DGELU_C8 = 13,       // out0 = dH = acc · GeLU′(H̃), out1 = Y = GeLU(H̃), H̃ from c8
+    EPI_DGELU_C8_TANH = 14,
 };
 
 // Epilogue classes: activation forward (two outputs), activation backward
 // (reads the saved pre-activation), and the tanh forms of both.
 template <int EPI>
 struct EpiTraits {
-    static constexpr bool kAct = (EPI == EPI_GELU || EPI == EPI_GELU_TANH);
-    static constexpr bool kDAct = (EPI == EPI_DGELU || EPI == EPI_DGELU_TANH);
-    static constexpr bool kTanh = (EPI == EPI_GELU_TANH || EPI == EPI_DGELU_TANH);
-    static constexpr bool kBias = (EPI == EPI_BIAS) || kAct;
+    static constexpr bool kAct = (EPI == EPI_GELU || EPI == EPI_GELU_TANH || EPI == EPI_GELU_ADD ||
+                                  EPI == EPI_GELU_ADD_TANH);
+    static constexpr bool kC8In = (EPI == EPI_DGELU_C8 || EPI == EPI_DGELU_C8_TANH);
+    static constexpr bool kC8Out = (EPI == EPI_GELU_C8 || EPI == EPI_GELU_C8_TANH);
+    static constexpr bool kDAct = (EPI == EPI_DGELU || EPI == EPI_DGELU_TANH) || kC8In;
+    static constexpr bool kActOnly = (EPI == EPI_ACT_ADD || EPI == EPI_ACT_ADD_TANH) || kC8Out;  // one output
+    static constexpr bool kTanh = (EPI == EPI_GELU_TANH || EPI == EPI_DGELU_TANH || EPI == EPI_ACT_ADD_TANH ||
+                                   EPI == EPI_GELU_ADD_TANH || EPI == EPI_GELU_C8_TANH ||
+                                   EPI == EPI_DGELU_C8_TANH);
+    static constexpr bool kResid = (EPI == EPI_ADD || EPI == EPI_ACT_ADD || EPI == EPI_ACT_ADD_TANH ||
+                                    EPI == EPI_GELU_ADD || EPI == EPI_GELU_ADD_TANH);
+    static constexpr bool kBias = (EPI == EPI_BIAS || EPI == EPI_ADD) || kAct || kActOnly;
+    static constexpr bool kTwo = kAct || kC8In;  // two outputs stored through the tensor maps
+    // the epilogue evaluates the activation or its derivative (its relay has no split path)
+    static constexpr bool kMath = kAct || kDAct || kActOnly;
 };
 
 // Work-unit schedules (see next_unit).
@@ -77,6 +100,12 @@ struct GemmArgs {
     int64_t ld_out;        // row stride (elements) of out0, out1 and aux
     const __nv_bfloat16* bias;
     const __nv_bfloat16* aux;
+    const __nv_bfloat16* resid;  // kResid epilogues: M × N, row stride ld_out; may be null, may be the output
+    // 8-bit checkpoint (kC8Out writes it, kC8In reads it): M rows of c8_ld bytes
+    // (a multiple of 32), and the scale bytes, one row of M per 32 columns
+    uint8_t* c8;
+    uint8_t* c8_scale;
+    int64_t c8_ld;
     uint64_t wait_limit_ns;
     // GeLU′ epilogues with the relay: if set, column sums of the stored (bf16)
     // output go to colsum_out[r·N + col] (fp32), one row r per 64 rows a
@@ -696,6 +725,28 @@ __device__ __forceinline__ void act_fast_x2(float x0, float x1, float& y0, float
     }
 }
 
+// Activation and derivative of two values at once, from one evaluation of
+// their common part (Φ and exp(−x²/2), or the logistic function).
+template <int EPI>
+__device__ __forceinline__ void act_both_fast_x2(float x0, float x1, float& y0, float& y1, float& d0,
+                                                 float& d1) {
+    const uint64_t x = f2_pack(x0, x1);
+    if constexpr (EpiTraits<EPI>::kTanh) {
+        const uint64_t x2 = f2_mul(x, x);
+        const uint64_t s = logistic_2u_x2(x, x2);
+        const uint64_t du2 = f2_fma(x2, f2_splat(0.21406445f), f2_splat(1.5957691f));
+        const uint64_t one_minus_s = f2_fma(s, f2_splat(-1.0f), f2_splat(1.0f));
+        const uint64_t xs = f2_mul(x, s);
+        f2_unpack(f2_fma(f2_mul(xs, one_minus_s), du2, s), d0, d1);
+        f2_unpack(xs, y0, y1);
+    } else {
+        uint64_t cdf, g;
+        normal_cdf_and_gauss_x2(x, x0, x1, cdf, g);
+        f2_unpack(f2_fma(f2_mul(x, f2_splat(0.39894228040143268f)), g, cdf), d0, d1);
+        f2_unpack(f2_mul(x, cdf), y0, y1);
+    }
+}
+
 template <int EPI>
 __device__ __forceinline__ void act_grad_fast_x2(float x0, float x1, float& d0, float& d1) {
     if constexpr (EpiTraits<EPI>::kTanh) {
@@ -787,6 +838,48 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& g, const CUtensor
     } else {
         uint4 o0[4], o1[4];
         const int64_t off = static_cast<int64_t>(row) * g.ld_out + col0;
+        // 8-bit checkpoint: this lane's row of the chunk is one block of 32
+        // columns, so its scale needs no exchange between lanes. Columns beyond
+        // N hold zeros (their operand columns are read as zero, no bias).
+        uint32_t codes[8];
+        float c8s = 0.0f;
+        if constexpr (EpiTraits<EPI>::kC8Out) {
+            float h[32];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float bb[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+                if (g.bias != nullptr && col0 + 8 * q < N)
+                    unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(g.bias + col0 + 8 * q)), bb);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) h[8 * q + i] = __uint_as_float(acc[8 * q + i]) + bb[i];
+            }
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) top = max_nan(top, fabsf(h[i]));
+            const uint32_t sb = c8_scale_byte(top);
+            const float inv = c8_inverse(sb);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                codes[i] = sb == kC8NaN ? 0u : c8_pack4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3], inv);
+            if (row < M && col0 < N) {
+                uint4* dst = reinterpret_cast<uint4*>(g.c8 + static_cast<int64_t>(row) * g.c8_ld + col0);
+                dst[0] = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+                dst[1] = make_uint4(codes[4], codes[5], codes[6], codes[7]);
+                g.c8_scale[static_cast<int64_t>(col0 / kC8Block) * M + row] = static_cast<uint8_t>(sb);
+            }
+        }
+        if constexpr (EpiTraits<EPI>::kC8In) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) codes[i] = 0u;
+            if (row < M && col0 < N) {
+                const uint4* src =
+                    reinterpret_cast<const uint4*>(g.c8 + static_cast<int64_t>(row) * g.c8_ld + col0);
+                const uint4 a = __ldg(src), b = __ldg(src + 1);
+                codes[0] = a.x; codes[1] = a.y; codes[2] = a.z; codes[3] = a.w;
+                codes[4] = b.x; codes[5] = b.y; codes[6] = b.z; codes[7] = b.w;
+                c8s = c8_scale(__ldg(g.c8_scale + static_cast<int64_t>(col0 / kC8Block) * M + row));
+            }
+        }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             const int c = col0 + 8 * q;
@@ -801,7 +894,21 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& g, const CUtensor
                     for (int i = 0; i < 8; ++i) v[i] += bb[i];
                 }
             }
-            if constexpr (EpiTraits<EPI>::kDAct) {
+            if constexpr (EpiTraits<EPI>::kC8In) {
+                float hh[8], y[8];
+                c8_unpack4(codes[2 * q], c8s, hh);
+                c8_unpack4(codes[2 * q + 1], c8s, hh + 4);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    float d0, d1;
+                    act_both_fast_x2<EPI>(hh[i], hh[i + 1], y[i], y[i + 1], d0, d1);
+                    f2_unpack(f2_mul(f2_pack(v[i], v[i + 1]), f2_pack(d0, d1)), v[i], v[i + 1]);
+                }
+                o1[q].x = pack_bf16x2(y[0], y[1]);
+                o1[q].y = pack_bf16x2(y[2], y[3]);
+                o1[q].z = pack_bf16x2(y[4], y[5]);
+                o1[q].w = pack_bf16x2(y[6], y[7]);
+            } else if constexpr (EpiTraits<EPI>::kDAct) {
                 float hh[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                 if (row < M && c < N)
                     unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(g.aux + off + 8 * q)), hh);
@@ -812,6 +919,20 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& g, const CUtensor
                     f2_unpack(f2_mul(f2_pack(v[i], v[i + 1]), f2_pack(d0, d1)), v[i], v[i + 1]);
                 }
             }
+            float res[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            if constexpr (EpiTraits<EPI>::kResid) {
+                // an ordinary load: resid may be the output this kernel writes
+                if (g.resid != nullptr && row < M && c < N)
+                    unpack_bf16x8(*reinterpret_cast<const uint4*>(g.resid + off + 8 * q), res);
+            }
+            if constexpr (EpiTraits<EPI>::kActOnly) {
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) act_fast_x2<EPI>(v[i], v[i + 1], v[i], v[i + 1]);
+            }
+            if constexpr (EpiTraits<EPI>::kResid && !EpiTraits<EPI>::kAct) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] += res[i];
+            }
             o0[q].x = pack_bf16x2(v[0], v[1]);
             o0[q].y = pack_bf16x2(v[2], v[3]);
             o0[q].z = pack_bf16x2(v[4], v[5]);
@@ -820,6 +941,10 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& g, const CUtensor
                 float y[8];
 #pragma unroll
                 for (int i = 0; i < 8; i += 2) act_fast_x2<EPI>(v[i], v[i + 1], y[i], y[i + 1]);
+                if constexpr (EpiTraits<EPI>::kResid) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) y[i] += res[i];
+                }
                 o1[q].x = pack_bf16x2(y[0], y[1]);
                 o1[q].y = pack_bf16x2(y[2], y[3]);
                 o1[q].z = pack_bf16x2(y[4], y[5]);
@@ -835,13 +960,13 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& g, const CUtensor
         for (int q = 0; q < 4; ++q) {
             const uint32_t a = lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
             st_shared_v4(slot + a, o0[q]);
-            if constexpr (EpiTraits<EPI>::kAct) st_shared_v4(slot + 2048 + a, o1[q]);
+            if constexpr (EpiTraits<EPI>::kTwo) st_shared_v4(slot + 2048 + a, o1[q]);
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && any) {
             tma_store_3d(tmO0, slot, col0, row0, 0);
-            if constexpr (EpiTraits<EPI>::kAct) tma_store_3d(tmO1, slot + 2048, col0, row0, 0);
+            if constexpr (EpiTraits<EPI>::kTwo) tma_store_3d(tmO1, slot + 2048, col0, row0, 0);
             bulk_commit();
         }
         if (DBL && any) sbuf ^= 1u;
@@ -889,7 +1014,7 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& g, const CUtensor
 // whole-tile path too). Their launches always run whole tiles (the host keeps
 // them so), and the split path is compiled out of them.
 template <int EPI, bool RELAY>
-constexpr bool kSplittable = !((EpiTraits<EPI>::kDAct || EpiTraits<EPI>::kAct) && RELAY);
+constexpr bool kSplittable = !(EpiTraits<EPI>::kMath && RELAY);
 
 template <int BN, int EPI, bool PAIR, bool RELAY, bool DBL = false>
 __device__ __forceinline__ void epilogue_role(const GemmArgs& g, const CUtensorMap* tmO0,
@@ -912,7 +1037,7 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& g, const CUtensorM
     const uint32_t partner_slot = smem_u32(sEpi + kSlotsPerWarp * (4 * half + quad) * kEpiSlotBytes);
     if (lane == 0 && !relay) {
         tma_prefetch_desc(tmO0);
-        if (EpiTraits<EPI>::kAct || g.second) tma_prefetch_desc(tmO1);
+        if (EpiTraits<EPI>::kTwo || g.second) tma_prefetch_desc(tmO1);
     }
     uint32_t xcount = 0;
     bool stored = false;  // a relay warp has bulk stores of a split tile in flight

@@ -28,8 +28,10 @@
 
 #include "../../include/tpmlp.h"
 #include "aux_kernels.cuh"
+#include "fused_kernels.cuh"
 #include "gemm_tc.cuh"
 #include "gemm_tc2.cuh"
+#include "norm.cuh"
 #include "simt.cuh"
 
 namespace tpmlp {
@@ -49,9 +51,9 @@ struct DeviceInfo {
     bool init = false;
     int cc_major = 0;
     int num_sms = 0;
-    bool attr_set[128] = {};       // per one-CTA tensor-core kernel instantiation
-    bool attr_set_pair[128] = {};  // per CTA-pair kernel instantiation
-    int max_pairs[128] = {};       // co-resident CTA pairs per pair-kernel instantiation
+    bool attr_set[256] = {};       // per one-CTA tensor-core kernel instantiation
+    bool attr_set_pair[256] = {};  // per CTA-pair kernel instantiation
+    int max_pairs[256] = {};       // co-resident CTA pairs per pair-kernel instantiation
 };
 DeviceInfo g_dev[kMaxDevices];
 std::mutex g_dev_mutex;
@@ -131,7 +133,7 @@ template <int EPI>
 bool make_out_maps(CUtensorMap* o0, CUtensorMap* o1, const GemmArgs& g, int M, int N) {
     const bool f32 = (EPI == EPI_F32);
     if (!make_out_map(o0, g.out0, M, N, f32)) return false;
-    if (EpiTraits<EPI>::kAct) return make_out_map(o1, g.out1, M, N, false);
+    if (EpiTraits<EPI>::kTwo) return make_out_map(o1, g.out1, M, N, false);
     *o1 = *o0;
     return true;
 }
@@ -174,7 +176,8 @@ tpmlp_status launch_dep(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sm
 
 enum Kind : int {
     K_F1 = 0, K_F2, K_B1_DB, K_B2, K_B2_DA, K_B3, K_B4, K_B34, K_B5, K_MISC,
-    K_L_FWD, K_L_DB, K_L_DW, K_L_DX, K_RECOMP, K_CTR, K_B12, K_COUNT
+    K_L_FWD, K_L_DB, K_L_DW, K_L_DX, K_RECOMP, K_CTR, K_B12, K_L_DH, K_N_FWD, K_N_BWD, K_N_DGB,
+    K_C8, K_COUNT
 };
 const char* const kKindNames[K_COUNT] = {
     "F1.col_gemm_bias_gelu", "F2.row_gemm_shard_sum", "B1.db_colsum",
@@ -182,6 +185,8 @@ const char* const kKindNames[K_COUNT] = {
     "B3+B4.wgrad_dB_dA",     "B5.dgrad_dX_shard_sum", "misc",
     "L.fwd_gemm_bias",       "L.dbias_colsum",        "L.wgrad_dW",      "L.dgrad_dX",
     "R.recompute_activation", "S.counter_reset",  "B1+B2.db_da_colsum",
+    "L.act_grad_dH",          "N.norm_fwd",       "N.norm_bwd",          "N.norm_dgamma_dbeta",
+    "R.ckpt8",
 };
 
 struct KindTotals {
@@ -239,7 +244,7 @@ tpmlp_status timed(int kind, double flops, double bytes, cudaStream_t st, Fn&& f
 
 // ------------------------------------------------------ tensor-core launches
 
-// Index of a tensor-core kernel instantiation (0..95) for per-device caches.
+// Index of a tensor-core kernel instantiation (0..239) for per-device caches.
 template <int BN, bool A_MN, bool B_MN, int EPI, bool RELAY, bool LONG = false>
 constexpr int kernel_id() {
     static_assert(BN == 256, "the launchers use 256-column tiles");
@@ -372,7 +377,7 @@ tpmlp_status gemm_tc2_launch(const void* Aop, const void* Bop, int M, int N, int
     CUtensorMap tmA2 = tmA, tmB2 = tmB;
     if (second != nullptr) {
         // the second product's output takes the second output map
-        if constexpr (EpiTraits<EPI>::kAct) return TPMLP_ERR_INVALID;
+        if constexpr (EpiTraits<EPI>::kTwo) return TPMLP_ERR_INVALID;
         const SecondProduct& q = *second;
         const bool ok2 = (A_MN ? make_map(&tmA2, q.A, K, q.M, 64) : make_map(&tmA2, q.A, q.M, K, kBM)) &&
                          (B_MN ? make_map(&tmB2, q.B, K, q.N, 64) : make_map(&tmB2, q.B, q.N, K, BN / 2)) &&
@@ -436,8 +441,12 @@ template <int EPI>
 double gemm_bytes(double M, double N, double K) {
     double b = 2.0 * (M * K + K * N);
     if (EpiTraits<EPI>::kAct) b += 2.0 * 2.0 * M * N;
-    if (EPI == EPI_BIAS) b += 2.0 * M * N;
-    if (EpiTraits<EPI>::kDAct) b += 2.0 * 2.0 * M * N;
+    if (EPI == EPI_BIAS || (EpiTraits<EPI>::kActOnly && !EpiTraits<EPI>::kC8Out)) b += 2.0 * M * N;
+    if (EPI == EPI_ADD) b += 2.0 * M * N;
+    if (EpiTraits<EPI>::kResid) b += 2.0 * M * N;
+    if (EpiTraits<EPI>::kC8Out) b += (2.0 + 33.0 / 32.0) * M * N;
+    if (EpiTraits<EPI>::kC8In) b += (4.0 + 33.0 / 32.0) * M * N;
+    else if (EpiTraits<EPI>::kDAct) b += 2.0 * 2.0 * M * N;
     if (EPI == EPI_F32) b += 4.0 * M * N;
     return b;
 }
@@ -505,7 +514,7 @@ tpmlp_status gemm_tc(int kind, const void* Aop, const void* Bop, int M, int N, i
     return timed(kind, 2.0 * M * N * K, gemm_bytes<EPI>(M, N, K), st, [&] {
         const int k_per_unit = req.kind == SCHED_GROUPS && req.groups > 1 ? K / req.groups : K;
         const int threshold =
-            (EpiTraits<EPI>::kAct || EpiTraits<EPI>::kDAct) ? kRelayMinKAct : kRelayMinKPlain;
+            EpiTraits<EPI>::kMath ? kRelayMinKAct : kRelayMinKPlain;
         const int64_t units = pair_tiles(M, N) * (req.kind == SCHED_GROUPS ? req.groups : 1);
         if (k_per_unit < threshold || (!EpiTraits<EPI>::kDAct && !relay_has_work(M, units)))
             return gemm_tc_pick<BN, A_MN, B_MN, EPI, false>(Aop, Bop, M, N, K, req, g, st);
@@ -513,16 +522,16 @@ tpmlp_status gemm_tc(int kind, const void* Aop, const void* Bop, int M, int N, i
     });
 }
 
-// Two products of the same kernel (fp32 epilogue) and K in one launch, as
-// one list of whole tiles on the CTA pairs (both M > 128): the second's
-// tiles follow the first's, so a short product no longer leaves half the
-// GPU idle for its whole duration.
-template <int BN, bool A_MN, bool B_MN>
+// Two products of the same kernel (one output; fp32, or EPI_BIAS without a
+// bias for bf16) and K in one launch, as one list of whole tiles on the CTA
+// pairs (both M > 128): the second's tiles follow the first's, so a short
+// product no longer leaves half the GPU idle for its whole duration.
+template <int BN, bool A_MN, bool B_MN, int EPI = EPI_F32>
 tpmlp_status gemm_tc_grouped(int kind, const void* A0, const void* B0, int M0, int N0, void* out0,
                              const void* A1, const void* B1, int M1, int N1, void* out1, int K,
                              cudaStream_t st) {
     const double flops = 2.0 * (double(M0) * N0 + double(M1) * N1) * K;
-    const double bytes = gemm_bytes<EPI_F32>(M0, N0, K) + gemm_bytes<EPI_F32>(M1, N1, K);
+    const double bytes = gemm_bytes<EPI>(M0, N0, K) + gemm_bytes<EPI>(M1, N1, K);
     return timed(kind, flops, bytes, st, [&] {
         GemmArgs g{};
         g.out0 = out0;
@@ -530,9 +539,9 @@ tpmlp_status gemm_tc_grouped(int kind, const void* A0, const void* B0, int M0, i
         const SchedReq req;  // whole tiles, static (fp32 outputs: no long-product variant)
         const SecondProduct second{A1, B1, M1, N1, out1};
         if (K < kRelayMinKPlain || !relay_has_work(M0, pair_tiles(M0, N0) + pair_tiles(M1, N1)))
-            return gemm_tc2_launch<BN, A_MN, B_MN, EPI_F32, false>(A0, B0, M0, N0, K, req, g, st,
+            return gemm_tc2_launch<BN, A_MN, B_MN, EPI, false>(A0, B0, M0, N0, K, req, g, st,
                                                                  &second);
-        return gemm_tc2_launch<BN, A_MN, B_MN, EPI_F32, true>(A0, B0, M0, N0, K, req, g, st,
+        return gemm_tc2_launch<BN, A_MN, B_MN, EPI, true>(A0, B0, M0, N0, K, req, g, st,
                                                             &second);
     });
 }
@@ -736,9 +745,9 @@ int64_t clamp_grid(int64_t blocks, int64_t cap) {
     return blocks < 1 ? 1 : blocks;
 }
 
-template <typename T>
+template <typename T, typename O>
 tpmlp_status colsum_launch(const T* X, int64_t R, int64_t C, int64_t chunks, float* partial,
-                           float* out, cudaStream_t st) {
+                           O* out, cudaStream_t st) {
     dim3 grid(static_cast<unsigned>((C + 255) / 256), static_cast<unsigned>(chunks));
     dim3 block(32, 8);
     const tpmlp_status s =
@@ -748,14 +757,14 @@ tpmlp_status colsum_launch(const T* X, int64_t R, int64_t C, int64_t chunks, flo
             : launch_dep(colsum_partial_kernel<T, false>, grid, block, 0, st, X, R, C,
                          kColsumRowsPerChunk, partial);
     if (s != TPMLP_OK) return s;
-    return launch_dep(colsum_final_kernel, dim3(static_cast<unsigned>((C + 31) / 32)), dim3(32, 8), 0,
+    return launch_dep(colsum_final_kernel<O>, dim3(static_cast<unsigned>((C + 31) / 32)), dim3(32, 8), 0,
                       st, static_cast<const float*>(partial), static_cast<int>(chunks), C, out);
 }
 
 // out = 1ᵀ·X for X: R × C; algorithmic bytes = X read once + out written.
-template <typename T>
+template <typename T, typename O>
 tpmlp_status colsum(int kind, const T* X, int64_t R, int64_t C, int64_t chunks, float* partial,
-                    float* out, cudaStream_t st) {
+                    O* out, cudaStream_t st) {
     return timed(kind, 0.0, sizeof(T) * double(R) * C + 4.0 * C, st,
                  [&] { return colsum_launch(X, R, C, chunks, partial, out, st); });
 }
@@ -763,9 +772,9 @@ tpmlp_status colsum(int kind, const T* X, int64_t R, int64_t C, int64_t chunks, 
 // Both bias gradients' column sums in two launches instead of four: pass 1
 // over X1 (R × C1) and X2 (R × C2) in one grid, then pass 2 of both. Each
 // column's sum is computed exactly as colsum computes it.
-template <typename T>
-tpmlp_status colsum2(int kind, const T* X1, int64_t C1, float* partial1, float* out1, const T* X2,
-                     int64_t C2, float* partial2, float* out2, int64_t R, int64_t chunks,
+template <typename T, typename O>
+tpmlp_status colsum2(int kind, const T* X1, int64_t C1, float* partial1, O* out1, const T* X2,
+                     int64_t C2, float* partial2, O* out2, int64_t R, int64_t chunks,
                      cudaStream_t st) {
     return timed(kind, 0.0, sizeof(T) * double(R) * (C1 + C2) + 4.0 * (C1 + C2), st, [&] {
         dim3 grid(static_cast<unsigned>((C1 + 255) / 256 + (C2 + 255) / 256),
@@ -777,7 +786,7 @@ tpmlp_status colsum2(int kind, const T* X1, int64_t C1, float* partial1, float* 
                 : launch_dep(colsum_partial2_kernel<T, false>, grid, dim3(32, 8), 0, st, X1, C1,
                              partial1, X2, C2, partial2, R, kColsumRowsPerChunk);
         if (s != TPMLP_OK) return s;
-        return launch_dep(colsum_final2_kernel,
+        return launch_dep(colsum_final2_kernel<O>,
                           dim3(static_cast<unsigned>((C1 + 31) / 32 + (C2 + 31) / 32)), dim3(32, 8), 0,
                           st, static_cast<const float*>(partial1), static_cast<int>(chunks), C1, out1,
                           static_cast<const float*>(partial2), static_cast<int>(chunks), C2, out2);
@@ -800,11 +809,12 @@ tpmlp_status colsum_first(int kind, const T* X, int64_t R, int64_t C, int64_t ch
 
 // Pass 2 of two sets of partials in one launch: out1[c] = Σ_r partial1[r][c]
 // over rows1 rows and out2 likewise, each in ascending r.
-tpmlp_status colsum_finish2(int kind, const float* partial1, int64_t rows1, int64_t C1, float* out1,
-                            const float* partial2, int64_t rows2, int64_t C2, float* out2,
+template <typename O>
+tpmlp_status colsum_finish2(int kind, const float* partial1, int64_t rows1, int64_t C1, O* out1,
+                            const float* partial2, int64_t rows2, int64_t C2, O* out2,
                             cudaStream_t st) {
     return timed(kind, 0.0, 4.0 * (double(rows1) * C1 + double(rows2) * C2 + C1 + C2), st, [&] {
-        return launch_dep(colsum_final2_kernel,
+        return launch_dep(colsum_final2_kernel<O>,
                           dim3(static_cast<unsigned>((C1 + 31) / 32 + (C2 + 31) / 32)), dim3(32, 8), 0,
                           st, partial1, static_cast<int>(rows1), C1, out1, partial2,
                           static_cast<int>(rows2), C2, out2);
@@ -1523,6 +1533,8 @@ tpmlp_status tpmlp_plan_dynamic(int64_t T, int64_t h, int64_t F, int p, tpmlp_dt
 int tpmlp_version(void) { return 200; }
 
 }  // extern "C"
+
+#include "fused_ops.cuh"
 
 // ---------------------------------------------------------------------------
 // Backward without any caller-provided memory beyond inputs and outputs.
