@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libtpmlp.so")
 SOURCES = ["tpmlp.cu"]
 HEADERS = ["ptx.cuh", "ckpt8.cuh", "gemm_tc.cuh", "gemm_tc2.cuh", "aux_kernels.cuh", "simt.cuh",
-           "fused_kernels.cuh", "norm.cuh", "fused_ops.cuh"]
+           "fused_kernels.cuh", "gemm_few.cuh", "norm.cuh", "fused_ops.cuh"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include", "tpmlp.h")
 
 NVCC_FLAGS = [

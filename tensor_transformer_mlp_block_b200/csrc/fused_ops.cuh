@@ -224,6 +224,78 @@ tpmlp_status norm_bwd_impl(const void* dY, const void* X, const void* gamma, con
 
 // -------------------------------------------- linear layer, fused epilogue
 
+// CTAs of a cluster that share a tile's K range (gemm_few.cuh): as many as
+// keep two CTAs per SM resident and leave each at least two k-blocks.
+int few_split(int64_t tiles, int64_t k_blocks) {
+    int s = 1;
+    while (s < 8 && tiles * s * 2 <= 2 * plan_num_sms() && k_blocks >= 4 * s) s *= 2;
+    return s;
+}
+
+template <int TN>
+tpmlp_status gemm_few_launch(const void* X, const void* W, int T, int N, int K, FewArgs g, cudaStream_t st) {
+    using Cfg = FewCfg<TN>;
+    CUtensorMap tmW, tmX;
+    if (!make_map(&tmW, W, K, N, kBK) || !make_map(&tmX, X, T, K, TN)) return TPMLP_ERR_CUDA;
+    g.T = T;
+    g.N = N;
+    g.k_blocks = (K + kBK - 1) / kBK;
+    g.wait_limit_ns = g_wait_limit_ns.load();
+    auto kern = gemm_few_kernel<TN>;
+    {
+        std::lock_guard<std::mutex> lock(g_dev_mutex);
+        static bool set[kMaxDevices] = {};
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TPMLP_ERR_CUDA;
+        if (!set[dev]) {
+            if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::SMEM_BYTES) !=
+                cudaSuccess)
+                return TPMLP_ERR_CUDA;
+            set[dev] = true;
+        }
+    }
+    const int tn = (N + kFewCols - 1) / kFewCols, tt = (T + TN - 1) / TN;
+    const int S = few_split(int64_t(tn) * tt, g.k_blocks);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(tn * S), static_cast<unsigned>(tt));
+    cfg.blockDim = dim3(kFewThreads);
+    cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(S);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = g_overlap.load(std::memory_order_relaxed) ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmW, tmX, g, S);
+    g_launches.fetch_add(1, std::memory_order_relaxed);
+    if (e != cudaSuccess) cudaGetLastError();
+    return e == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
+}
+
+// Rows up to which the few-row kernel serves the forward.
+constexpr int64_t kFewMaxRows = 64;
+
+tpmlp_status linear_few(const void* X, const void* W, const void* bias, const void* R, void* H, void* Y, int T, int N,
+                        int K, tpmlp_activation act, cudaStream_t st) {
+    FewArgs g{};
+    g.act = static_cast<int>(act);
+    g.bias = static_cast<const bf16*>(bias);
+    g.resid = static_cast<const bf16*>(R);
+    g.H = static_cast<bf16*>(H);
+    g.Y = static_cast<bf16*>(Y);
+    const double bytes = 2.0 * (double(T) * K + double(K) * N + (1.0 + (R != nullptr) + (H != nullptr)) * T * N);
+    return timed(K_L_FWD, 2.0 * T * N * K, bytes, st, [&] {
+        if (T <= 16) return gemm_few_launch<16>(X, W, T, N, K, g, st);
+        if (T <= 32) return gemm_few_launch<32>(X, W, T, N, K, g, st);
+        if (T <= 64) return gemm_few_launch<64>(X, W, T, N, K, g, st);
+        return gemm_few_launch<128>(X, W, T, N, K, g, st);
+    });
+}
+
 // The forward's product with EPI (kResid) on the tensor cores.
 template <int EPI>
 tpmlp_status linear_ex_tc(const void* X, const void* W, int T, int N, int K, const SchedReq& req, const GemmArgs& g,
@@ -260,6 +332,7 @@ tpmlp_status linear_fwd_ex_impl(const void* X, const void* W, const void* bias, 
     if (pl.tc) {
         for (const void* q : {X, W, bias, R, static_cast<const void*>(H), static_cast<const void*>(Y)})
             if (q && !aligned16(q)) return TPMLP_ERR_ALIGN;
+        if (T <= kFewMaxRows) return linear_few(X, W, bias, R, H, Y, iT, iN, iK, act, st);
         // the relaying activation epilogues run whole tiles (kSplittable)
         const SchedReq req = (act != TPMLP_ACT_NONE && K >= kRelayMinKAct) ? SchedReq{} : pl.fwd;
         GemmArgs g{};

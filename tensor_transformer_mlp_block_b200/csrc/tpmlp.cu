@@ -29,6 +29,7 @@
 #include "../../include/tpmlp.h"
 #include "aux_kernels.cuh"
 #include "fused_kernels.cuh"
+#include "gemm_few.cuh"
 #include "gemm_tc.cuh"
 #include "gemm_tc2.cuh"
 #include "norm.cuh"
