@@ -164,8 +164,9 @@ tpmlp_status tp_linear_bwd(const void* dY, const void* X, const void* W, void* d
  *   input.
  * H: T×N output of dtype dt, the pre-activation the backward needs, or NULL
  *   (inference). With TPMLP_ACT_NONE it must be NULL.
- * Up to 64 rows (single tokens, small batches) the tensor-core path splits K
- * over a cluster of CTAs, so that reading W uses the whole GPU.
+ * Up to 128 rows (single tokens, small batches) the tensor-core path splits
+ * K over a cluster of CTAs, so that reading W uses the whole GPU; K is then
+ * summed in up to 8 consecutive parts, whatever the split policy.
  *
  * Backward, for the upstream gradient dY (T×N; R's gradient is dY itself):
  *   dH = dY ⊙ act′(H)        (T×N, dtype dt, rounded once; written to dH)

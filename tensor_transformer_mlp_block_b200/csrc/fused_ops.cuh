@@ -224,11 +224,17 @@ tpmlp_status norm_bwd_impl(const void* dY, const void* X, const void* gamma, con
 
 // -------------------------------------------- linear layer, fused epilogue
 
-// CTAs of a cluster that share a tile's K range (gemm_few.cuh): as many as
-// keep two CTAs per SM resident and leave each at least two k-blocks.
-int few_split(int64_t tiles, int64_t k_blocks) {
+// CTAs of a cluster that share a tile's K range (gemm_few.cuh): the power of
+// two up to 8 that fills the resident CTAs without a second wave and leaves
+// each at least two k-blocks. An SM streams about 64 GB/s however much its
+// ring holds, so what counts is that all of them load. Measured on B200 (µs,
+// S = 1 / 2 / 4 / 8): 24 rows, 16384 → 4096 (32 tiles) 82 / 45 / 27 / 24; 1
+// row, 4096 → 16384 (128 tiles) 24.0 / 23.9 / 27 / 34; 16 rows, 4096 → 1024
+// (8 tiles) 23 / 14 / 8.5 / 5.9. Clusters of 3, 5, 6 or 7 leave SMs idle and
+// gain nothing (1 row, 12288 → 12288: S = 2 52, S = 3 66).
+int few_split(int64_t tiles, int64_t k_blocks, int ctas_per_sm) {
     int s = 1;
-    while (s < 8 && tiles * s * 2 <= 2 * plan_num_sms() && k_blocks >= 4 * s) s *= 2;
+    while (s < 8 && tiles * s * 2 <= ctas_per_sm * plan_num_sms() && k_blocks >= 4 * s) s *= 2;
     return s;
 }
 
@@ -255,7 +261,7 @@ tpmlp_status gemm_few_launch(const void* X, const void* W, int T, int N, int K, 
         }
     }
     const int tn = (N + kFewCols - 1) / kFewCols, tt = (T + TN - 1) / TN;
-    const int S = few_split(int64_t(tn) * tt, g.k_blocks);
+    const int S = few_split(int64_t(tn) * tt, g.k_blocks, Cfg::CTAS);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(tn * S), static_cast<unsigned>(tt));
     cfg.blockDim = dim3(kFewThreads);
@@ -276,8 +282,11 @@ tpmlp_status gemm_few_launch(const void* X, const void* W, int T, int N, int K, 
     return e == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
 }
 
-// Rows up to which the few-row kernel serves the forward.
-constexpr int64_t kFewMaxRows = 64;
+// Rows up to which the few-row kernel serves the forward: one tile of 128.
+// Measured at 128 rows against the one-CTA kernel under its best schedule: 4096
+// → 4096 15.4 against 31.5 µs, 16384 → 4096 33 against 62, 4096 → 16384 34.5
+// against 35.3. A second tile would read W again.
+constexpr int64_t kFewMaxRows = 128;
 
 tpmlp_status linear_few(const void* X, const void* W, const void* bias, const void* R, void* H, void* Y, int T, int N,
                         int K, tpmlp_activation act, cudaStream_t st) {

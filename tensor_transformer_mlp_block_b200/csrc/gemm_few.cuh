@@ -7,8 +7,8 @@
 // of W per tile as the tensor cores' 128 rows (W [K][N] is read MN-major, as it
 // lies) and TN rows of X as their N, and the tile's K range is split over a
 // cluster of S CTAs. Each CTA streams its part of W through a shared-memory
-// ring, two CTAs to an SM; the fp32 partial tiles meet in distributed shared
-// memory and are added in ascending k by the CTA that owns the columns, so
+// ring. Every CTA of the cluster owns ⌈128/S⌉ of the tile's columns: the others store their fp32 partial sums of them straight into its
+// shared memory, and after one cluster barrier it adds them in ascending k. So
 // nothing goes through global memory, no counters are needed, and the result
 // does not depend on timing.
 //
@@ -29,13 +29,15 @@ struct FewCfg {
     static constexpr int W_BYTES = kFewCols * kBK * 2;
     static constexpr int X_BYTES = TN * kBK * 2;
     static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-    // two CTAs per SM: at most 110 KB each
-    static constexpr int STAGES = 110000 / STAGE_BYTES;
+    // partial sums of this CTA's columns: [rank][row][column], S·⌈128/S⌉ <= 135
+    static constexpr int PART_BYTES = TN * 136 * 4;
+    // Two CTAs per SM (at most 113 KB each), so that one's prologue and sums
+    // run beside the other's loads; a tile of 128 rows leaves room for one.
+    static constexpr int CTAS = TN <= 64 ? 2 : 1;
+    static constexpr int STAGES = ((CTAS == 2 ? 114000 : 228000) - PART_BYTES) / STAGE_BYTES;
     static constexpr int TMEM_COLS = TN < 32 ? 32 : TN;
-    static constexpr int LD = TN + 1;  // row stride (floats) of the partial tile in shared memory
     static constexpr int BAR_BYTES = 8 * (2 * STAGES + 1) + 16;
-    static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + BAR_BYTES;
-    static_assert(kFewCols * LD * 4 <= STAGES * STAGE_BYTES, "the partial tile reuses the ring");
+    static constexpr int SMEM_BYTES = 1024 + PART_BYTES + STAGES * STAGE_BYTES + BAR_BYTES;
 };
 
 struct FewArgs {
@@ -62,7 +64,7 @@ __device__ __forceinline__ void few_store(const FewArgs& g, int t, int n, float 
 
 // Grid (tiles of W's columns × S, tiles of TN rows), cluster (S, 1).
 template <int TN>
-__global__ void __launch_bounds__(kFewThreads, 2)
+__global__ void __launch_bounds__(kFewThreads, FewCfg<TN>::CTAS)
     gemm_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                     const FewArgs g, int S) {
     using C = FewCfg<TN>;
@@ -74,7 +76,8 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                                                ~static_cast<uintptr_t>(1023));
     uint8_t* sW = smem;
     uint8_t* sX = smem + STAGES * C::W_BYTES;
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE_BYTES);
+    float* parts = reinterpret_cast<float*>(smem + STAGES * C::STAGE_BYTES);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + STAGES * C::STAGE_BYTES + C::PART_BYTES);
     uint64_t* full = bars;
     uint64_t* empty = bars + STAGES;
     uint64_t* done = bars + 2 * STAGES;
@@ -168,24 +171,29 @@ __global__ void __launch_bounds__(kFewThreads, 2)
         }
         __syncwarp();
     } else {
+        const int quad = warp & 3;
+        const int c = quad * 32 + lane;  // column of W within the tile
+        const int rows = min(TN, g.T - t0);
+        if (g.resid != nullptr && (lane & 15) == 0 && n0 + c < g.N) {
+            // the residual's first touch of memory runs beside the product
+            for (int t = rank; t < rows; t += S)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(g.resid + static_cast<int64_t>(t0 + t) * g.N + n0 + c));
+        }
         // every lane waits and the warp goes on only together (.sync.aligned loads)
         ok = mbar_wait_bounded(smem_u32(done), 0, abort, limit);
-        ok = __all_sync(0xffffffffu, ok) && !*abort;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) raise_timeout(abort);
         if (ok) {
             tc_fence_after();
-            const int quad = warp & 3;
-            const int c = quad * 32 + lane;  // column of W within the tile
             const int n = n0 + c;
             const uint32_t src = tmem + (static_cast<uint32_t>(quad * 32) << 16);
-            const int rows = min(TN, g.T - t0);
-            float* part = reinterpret_cast<float*>(smem) + c * C::LD;
             float bias = 0.0f;
             if (S == 1 && g.bias != nullptr && n < g.N) bias = __bfloat162float(g.bias[n]);
+            // the owner of column c, and where this rank's sums of it go
+            const int cols = (kFewCols + S - 1) / S;
+            const uint32_t dst = S > 1 ? mapa_shared(smem_u32(parts + rank * TN * cols + c % cols), c / cols) : 0u;
 #pragma unroll 1
-            for (int j = 0; j < TN; j += 16) {
-                if (j >= rows) break;
+            for (int j = 0; j < rows; j += 16) {
                 uint32_t v[16];
                 tmem_ld_32x32b_x16(src + j, v);
                 tmem_wait_ld();
@@ -194,41 +202,36 @@ __global__ void __launch_bounds__(kFewThreads, 2)
                     for (int i = 0; i < 16; ++i)
                         if (j + i < rows && n < g.N) few_store(g, t0 + j + i, n, __uint_as_float(v[i]), bias);
                 } else {
-                    // the MMAs that read the ring have completed, and so have the
-                    // copies into it: the partial tile may take its place
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) part[j + i] = __uint_as_float(v[i]);
+                    for (int i = 0; i < 16; ++i)
+                        if (j + i < rows) st_shared_cluster_u32(dst + 4 * (j + i) * cols, v[i]);
                 }
             }
         }
     }
     tc_fence_before();
     if (S > 1) {
-        cluster_sync();  // every rank's partial tile is in its shared memory
+        cluster_sync();  // every rank's sums of this rank's columns have arrived
         if (warp >= 2 && ok) {
-            // this rank's columns: 128/S of them, all rows, the ranks in ascending k
-            const int cols = kFewCols / S;
+            const int cols = (kFewCols + S - 1) / S;
             const int rows = min(TN, g.T - t0);
-            const int e0 = static_cast<int>(threadIdx.x) - 64;
-            const int c = rank * cols + e0 % cols;  // 128 threads, cols divides 128
+            const int e = static_cast<int>(threadIdx.x) - 64;
+            const int per = 128 / cols;  // rows at a time; the last threads may have none
+            const int c = rank * cols + e % cols;
             const int n = n0 + c;
-            if (n < g.N) {
+            if (n < g.N && c < kFewCols && e < per * cols) {
                 const float bias = g.bias != nullptr ? __bfloat162float(g.bias[n]) : 0.0f;
-                const uint32_t base = smem_u32(reinterpret_cast<float*>(smem) + c * C::LD);
-                for (int t = e0 / cols; t < rows; t += 128 / cols) {
-                    float part[8];
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        if (q < S) part[q] = ld_shared_cluster_f32(mapa_shared(base + 4 * t, q));
-                    float v = part[0];
+                const float* p = parts + e % cols;
+#pragma unroll 4
+                for (int t = e / cols; t < rows; t += per) {
+                    float v = p[t * cols];
 #pragma unroll
                     for (int q = 1; q < 8; ++q)
-                        if (q < S) v += part[q];
+                        if (q < S) v += p[(q * TN + t) * cols];
                     few_store(g, t0 + t, n, v, bias);
                 }
             }
         }
-        cluster_sync();  // no CTA leaves while its tile is still read
     } else {
         __syncthreads();
     }

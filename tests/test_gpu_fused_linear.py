@@ -145,7 +145,7 @@ def test_splits_and_schedules(policy, split, act):
     assert binding.last_device_status() == binding.OK
 
 
-@pytest.mark.parametrize("T", [1, 40, 200, 2100])
+@pytest.mark.parametrize("T", [1, 40, 100, 200, 2100])
 @pytest.mark.parametrize("K", [64, 4096])
 def test_long_and_relayed_products(T, K):
     """K on both sides of the relaying epilogue's threshold, enough tiles for the long-product variant."""
