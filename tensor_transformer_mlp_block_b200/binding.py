@@ -520,12 +520,18 @@ def _take(t, name, shape, dtype, dev):
     return t.data_ptr()
 
 
-def _give(t, name, shape, dtype, dev):
-    """An output: the caller's, checked, or a new one."""
+def _give(t, name, shape, like, dtype=None):
+    """An output: the caller's, checked, or a new one on like's device (dtype:
+    like's if None)."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
-    _need(t, name, shape, dtype, dev)
+        return like.new_empty(shape, dtype=dtype)
+    _need(t, name, shape, like.dtype if dtype is None else dtype, like.device)
     return t
+
+
+def _stream_of(dev):
+    """Handle of the device's current stream."""
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _work(n, workspace, dev):
@@ -575,17 +581,14 @@ def layernorm_forward(X, gamma, beta, *, eps: float = 1e-5, stats: bool = True, 
     pb = _take(beta, "beta", (h,), dt, dev)
     with _scope(dev, stream):
         Y, mean, rstd = (None, None, None) if out is None else out
-        Y = _give(Y, "Y", (T, h), dt, dev)
+        Y = _give(Y, "Y", (T, h), X)
         if stats:
-            if mean is None and rstd is None:
-                # one allocation for both rows of statistics
-                mean, rstd = torch.empty((2, T), dtype=torch.float32, device=dev).unbind(0)
-            mean = _give(mean, "mean", (T,), torch.float32, dev)
-            rstd = _give(rstd, "rstd", (T,), torch.float32, dev)
+            mean = _give(mean, "mean", (T,), X, torch.float32)
+            rstd = _give(rstd, "rstd", (T,), X, torch.float32)
         else:
             mean = rstd = None
         st = lib().tp_layernorm_fwd(px, pg, pb, Y.data_ptr(), _ptr(mean), _ptr(rstd), T, h, eps, code,
-                                    torch.cuda.current_stream(dev).cuda_stream)
+                                    _stream_of(dev))
     _check(st, "tp_layernorm_fwd")
     return Y, mean, rstd
 
@@ -610,15 +613,13 @@ def layernorm_backward(dY, X, gamma, mean, rstd, *, residual_grad=None, out=None
     pd = _take(residual_grad, "residual_grad", (T, h), dt, dev)
     with _scope(dev, stream):
         dX, dgamma, dbeta = (None, None, None) if out is None else out
-        dX = _give(dX, "dX", (T, h), dt, dev)
-        if dgamma is None and dbeta is None:
-            dgamma, dbeta = torch.empty((2, h), dtype=f32, device=dev).unbind(0)
-        dgamma = _give(dgamma, "dgamma", (h,), f32, dev)
-        dbeta = _give(dbeta, "dbeta", (h,), f32, dev)
+        dX = _give(dX, "dX", (T, h), X)
+        dgamma = _give(dgamma, "dgamma", (h,), X, f32)
+        dbeta = _give(dbeta, "dbeta", (h,), X, f32)
         L = lib()
         ws, nb = _work(int(L.tpmlp_layernorm_workspace_size(T, h, code)), workspace, dev)
         st = L.tp_layernorm_bwd(py, px, pg, pm, pr, pd, dX.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(),
-                                T, h, code, ws.data_ptr(), nb, torch.cuda.current_stream(dev).cuda_stream)
+                                T, h, code, ws.data_ptr(), nb, _stream_of(dev))
     _check(st, "tp_layernorm_bwd")
     return dX, dgamma, dbeta
 
@@ -651,12 +652,12 @@ def fused_linear_forward(X, W, bias, p: int = 1, split: str = "columns", *, acti
     pb = _take(bias, "bias", (N,), dt, dev)
     pr = _take(residual, "residual", (T, N), dt, dev)
     with _scope(dev, stream):
-        Y = _give(out, "out", (T, N), dt, dev)
-        H = _give(hidden, "hidden", (T, N), dt, dev) if keep_hidden or hidden is not None else None
+        Y = _give(out, "out", (T, N), X)
+        H = _give(hidden, "hidden", (T, N), X) if keep_hidden or hidden is not None else None
         L = lib()
         ws, nb = _work(int(L.tpmlp_linear_ex_workspace_size(T, K, N, int(p), split_code, code)), workspace, dev)
         st = L.tp_linear_fwd_ex(px, pw, pb, pr, _ptr(H), Y.data_ptr(), T, K, N, int(p), split_code, code, act,
-                                ws.data_ptr(), nb, torch.cuda.current_stream(dev).cuda_stream)
+                                ws.data_ptr(), nb, _stream_of(dev))
     _check(st, "tp_linear_fwd_ex")
     return Y if H is None else (Y, H)
 
@@ -682,15 +683,15 @@ def fused_linear_backward(dY, X, W, H=None, p: int = 1, split: str = "columns", 
     ph = _take(H, "H", (T, N), dt, dev)
     with _scope(dev, stream):
         dX, dW, db, dH = (tuple(out or ()) + (None,) * 4)[:4]
-        dX = _give(dX, "dX", (T, K), dt, dev)
-        dW = _give(dW, "dW", (K, N), grad_dtype, dev)
-        db = _give(db, "dbias", (N,), grad_dtype, dev)
-        dH = None if H is None else _give(dH, "dH", (T, N), dt, dev)
+        dX = _give(dX, "dX", (T, K), X)
+        dW = _give(dW, "dW", (K, N), X, grad_dtype)
+        db = _give(db, "dbias", (N,), X, grad_dtype)
+        dH = None if H is None else _give(dH, "dH", (T, N), X)
         L = lib()
         ws, nb = _work(int(L.tpmlp_linear_ex_workspace_size(T, K, N, int(p), split_code, code)), workspace, dev)
         st = L.tp_linear_bwd_ex(py, px, pw, ph, dX.data_ptr(), dW.data_ptr(), db.data_ptr(), _ptr(dH), T, K, N,
                                 int(p), split_code, code, gcode, act, ws.data_ptr(), nb,
-                                torch.cuda.current_stream(dev).cuda_stream)
+                                _stream_of(dev))
     _check(st, "tp_linear_bwd_ex")
     return dX, dW, db
 
@@ -714,10 +715,10 @@ def ckpt8_encode(H, *, out=None, stream=None):
     sc, ss = ckpt8_shapes(T, F)
     with _scope(dev, stream):
         C, S = (None, None) if out is None else out
-        C = _give(C, "C", sc, torch.int8, dev)
-        S = _give(S, "S", ss, torch.uint8, dev)
+        C = _give(C, "C", sc, H, torch.int8)
+        S = _give(S, "S", ss, H, torch.uint8)
         st = lib().tpmlp_ckpt8_encode(ph, C.data_ptr(), S.data_ptr(), T, F, code,
-                                      torch.cuda.current_stream(dev).cuda_stream)
+                                      _stream_of(dev))
     _check(st, "tpmlp_ckpt8_encode")
     return C, S
 
@@ -730,9 +731,9 @@ def ckpt8_decode(C, S, F: int, *, dtype=torch.bfloat16, out=None, stream=None):
     pc = _take(C, "C", sc, torch.int8, dev)
     ps = _take(S, "S", ss, torch.uint8, dev)
     with _scope(dev, stream):
-        H = _give(out, "out", (T, F), dtype if out is None else out.dtype, dev)
+        H = _give(out, "out", (T, F), C, dtype if out is None else out.dtype)
         st = lib().tpmlp_ckpt8_decode(pc, ps, H.data_ptr(), T, F, _dtype_code(H),
-                                      torch.cuda.current_stream(dev).cuda_stream)
+                                      _stream_of(dev))
     _check(st, "tpmlp_ckpt8_decode")
     return H
 
@@ -761,15 +762,15 @@ def forward_ckpt8(X, A, a, B, b, p: int, *, residual=None, activation: str = "ge
     sc, ss = ckpt8_shapes(T, F)
     with _scope(dev, stream):
         C, S, Z = (None, None, None) if out is None else out
-        C = _give(C, "C", sc, torch.int8, dev)
-        S = _give(S, "S", ss, torch.uint8, dev)
-        Z = _give(Z, "Z", (T, h), dt, dev)
-        Y = _give(scratch, "scratch", (T, F), dt, dev)
+        C = _give(C, "C", sc, X, torch.int8)
+        S = _give(S, "S", ss, X, torch.uint8)
+        Z = _give(Z, "Z", (T, h), X)
+        Y = _give(scratch, "scratch", (T, F), X)
         L = lib()
         ws, nb = _work(int(L.tpmlp_ckpt8_workspace_size(T, h, F, int(p), code)), workspace, dev)
         st = L.tp_mlp_fwd_ckpt8(px, pA, pa, pB, pb, pr, C.data_ptr(), S.data_ptr(), Y.data_ptr(), Z.data_ptr(),
                                 T, h, F, int(p), code, act, ws.data_ptr(), nb,
-                                torch.cuda.current_stream(dev).cuda_stream)
+                                _stream_of(dev))
     _check(st, "tp_mlp_fwd_ckpt8")
     return C, S, Z
 
@@ -794,7 +795,7 @@ def backward_ckpt8(dZ, X, A, B, C, S, p: int, *, activation: str = "gelu", grad_
     ps = _take(S, "S", ss, torch.uint8, dev)
     with _scope(dev, stream):
         given = out or {}
-        res = {name: _give(given.get(name), name, shp, d, dev)
+        res = {name: _give(given.get(name), name, shp, X, d)
                for name, shp, d in (("dX", (T, h), dt), ("dA", (h, F), grad_dtype), ("da", (F,), grad_dtype),
                                     ("dB", (F, h), grad_dtype), ("db", (h,), grad_dtype), ("dH", (T, F), dt),
                                     ("Y", (T, F), dt))}
@@ -803,7 +804,7 @@ def backward_ckpt8(dZ, X, A, B, C, S, p: int, *, activation: str = "gelu", grad_
         st = L.tp_mlp_bwd_ckpt8(pz, px, pA, pB, pc, ps, res["dX"].data_ptr(), res["dA"].data_ptr(),
                                 res["da"].data_ptr(), res["dB"].data_ptr(), res["db"].data_ptr(),
                                 res["dH"].data_ptr(), res["Y"].data_ptr(), T, h, F, int(p), code, gcode, act,
-                                ws.data_ptr(), nb, torch.cuda.current_stream(dev).cuda_stream)
+                                ws.data_ptr(), nb, _stream_of(dev))
     _check(st, "tp_mlp_bwd_ckpt8")
     return res
 

@@ -101,11 +101,96 @@ int64_t norm_bwd_blocks(int64_t T, const NormShape& s) {
     return std::max<int64_t>(1, std::min((T + s.rows - 1) / s.rows, plan_num_sms() * per_sm));
 }
 
+// Shape of the ring kernel (norm_bwd_ring_kernel) for rows of whole 16-byte
+// vectors: `elems` elements per thread, `threads` per row, `rows` groups per
+// block, `per_sm` blocks per SM, a ring of `stages` rows per group. threads =
+// 0: two rows of X, dY and dR do not fit a block's shared memory.
+struct NormRingShape {
+    int elems, threads, rows, per_sm, stages;
+};
+
+constexpr int kNormRingBytes = 224 * 1024;  // of shared memory per SM, for all blocks
+
+NormRingShape norm_ring_shape(int64_t h, int esize) {
+    NormRingShape s{0, 0, 1, 1, 0};
+    const int64_t stage = 3 * h * esize, gamma = h * esize, other = 2048;  // bytes
+    if (h <= 1024) {  // a warp per row
+        s.elems = h <= 256 ? 8 : h <= 512 ? 16 : 32;
+        s.threads = 32;
+        s.rows = kNormRows;
+        s.per_sm = 4;
+    } else {
+        s.elems = h <= 16 * 768 ? 16 : 32;
+        const int64_t t = ((h + s.elems - 1) / s.elems + 31) / 32 * 32;
+        if (t > (s.elems == 16 ? 768 : 512)) return NormRingShape{0, 0, 1, 1, 0};
+        s.threads = static_cast<int>(t);
+        s.per_sm = t <= 128 ? 4 : t <= 256 ? 2 : 1;
+    }
+    auto fit = [&] { return (kNormRingBytes / s.per_sm - gamma - other) / (stage * s.rows); };
+    while (s.per_sm > 1 && fit() < 3) --s.per_sm;
+    if (fit() < 2) return NormRingShape{0, 0, 1, 1, 0};
+    s.stages = static_cast<int>(std::min<int64_t>(fit(), 4));
+    return s;
+}
+
+int64_t norm_ring_blocks(int64_t T, const NormRingShape& s) {
+    return std::max<int64_t>(1, std::min<int64_t>((T + s.rows - 1) / s.rows, int64_t(plan_num_sms()) * s.per_sm));
+}
+
 size_t norm_workspace(int64_t T, int64_t h, tpmlp_dtype dt) {
     const int esize = dt == TPMLP_BF16 ? 2 : 4;
     int64_t blocks = norm_bwd_blocks(T, norm_shape(h, esize, false, true));
-    if (h % (16 / esize) == 0) blocks = std::max(blocks, norm_bwd_blocks(T, norm_shape(h, esize, true, true)));
+    if (h % (16 / esize) == 0) {
+        blocks = std::max(blocks, norm_bwd_blocks(T, norm_shape(h, esize, true, true)));
+        const NormRingShape ring = norm_ring_shape(h, esize);
+        if (ring.threads > 0) blocks = std::max(blocks, norm_ring_blocks(T, ring));
+    }
     return 2 * round256(static_cast<size_t>(blocks) * h * sizeof(float));
+}
+
+// Lets `kern` use up to kNormRingBytes of dynamic shared memory (once per device).
+template <auto KERNEL>
+tpmlp_status allow_ring_smem() {
+    static std::atomic<bool> set[kMaxDevices] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TPMLP_ERR_CUDA;
+    if (!set[dev].load()) {
+        if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRingBytes) != cudaSuccess)
+            return TPMLP_ERR_CUDA;
+        set[dev].store(true);
+    }
+    return TPMLP_OK;
+}
+
+template <typename T, int NV, bool WARP, int MAX_THREADS>
+tpmlp_status norm_ring_launch(const NormRingShape& s, const T* dY, const T* X, const T* gamma, const float* mean,
+                              const float* rstd, const T* dR, T* dX, float* pg, float* pb, int64_t blocks, int64_t R,
+                              int64_t h, cudaStream_t st) {
+    TPMLP_TRY((allow_ring_smem<norm_bwd_ring_kernel<T, NV, WARP, MAX_THREADS>>()));
+    // the rings, and gamma behind them
+    const size_t smem = (static_cast<size_t>(s.rows) * s.stages * (dR != nullptr ? 3 : 2) + 1) * h * sizeof(T);
+    return launch_dep(norm_bwd_ring_kernel<T, NV, WARP, MAX_THREADS>, dim3(static_cast<unsigned>(blocks)), dim3(s.threads, s.rows),
+                      smem, st, dY, X, gamma, mean, rstd, dR, dX, pg, pb, R, static_cast<int>(h),
+                      NormRing{s.stages, g_wait_limit_ns.load()});
+}
+
+template <typename T, bool WARP>
+tpmlp_status norm_ring_dispatch(const NormRingShape& s, const T* dY, const T* X, const T* gamma, const float* mean,
+                                const float* rstd, const T* dR, T* dX, float* pg, float* pb, int64_t blocks,
+                                int64_t R, int64_t h, cudaStream_t st) {
+    constexpr int kVec = 16 / sizeof(T);
+#define TPMLP_RING(NV, MAX) \
+    norm_ring_launch<T, NV, WARP, MAX>(s, dY, X, gamma, mean, rstd, dR, dX, pg, pb, blocks, R, h, st)
+    if constexpr (WARP) {
+        if (s.elems == 8) return TPMLP_RING(8 / kVec, 32 * kNormRows);
+        if (s.elems == 16) return TPMLP_RING(16 / kVec, 32 * kNormRows);
+        return TPMLP_RING(32 / kVec, 32 * kNormRows);
+    } else {
+        // 512 threads may take 128 registers each, 768 only 80
+        if (s.elems == 16) return s.threads <= 512 ? TPMLP_RING(16 / kVec, 512) : TPMLP_RING(16 / kVec, 768);
+        return TPMLP_RING(32 / kVec, 512);
+    }
+#undef TPMLP_RING
 }
 
 template <typename T, int VE, int NV>
@@ -199,7 +284,8 @@ tpmlp_status norm_bwd_impl(const void* dY, const void* X, const void* gamma, con
     const bool vec = h % (16 / sizeof(T)) == 0 && aligned16(dY) && aligned16(X) && aligned16(gamma) &&
                      aligned16(dR) && aligned16(dX);
     const NormShape s = norm_shape(h, sizeof(T), vec, true);
-    const int64_t blocks = norm_bwd_blocks(R, s);
+    const NormRingShape ring = vec ? norm_ring_shape(h, sizeof(T)) : NormRingShape{0, 0, 1, 1, 0};
+    const int64_t blocks = ring.threads > 0 ? norm_ring_blocks(R, ring) : norm_bwd_blocks(R, s);
     float* pg = static_cast<float*>(workspace);
     float* pb = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                          round256(static_cast<size_t>(blocks) * h * sizeof(float)));
@@ -210,6 +296,10 @@ tpmlp_status norm_bwd_impl(const void* dY, const void* X, const void* gamma, con
     T* dx = static_cast<T*>(dX);
     const double bytes = sizeof(T) * ((dR ? 4.0 : 3.0) * R * h + h) + 8.0 * R + 8.0 * blocks * h;
     TPMLP_TRY(timed(K_N_BWD, 0.0, bytes, st, [&]() -> tpmlp_status {
+        if (ring.threads == 32)
+            return norm_ring_dispatch<T, true>(ring, y, x, g, mean, rstd, d, dx, pg, pb, blocks, R, h, st);
+        if (ring.threads > 0)
+            return norm_ring_dispatch<T, false>(ring, y, x, g, mean, rstd, d, dx, pg, pb, blocks, R, h, st);
         if (s.threads == 0) {
             const dim3 cols(static_cast<unsigned>(blocks), static_cast<unsigned>((h + 255) / 256));
             TPMLP_TRY(launch_dep(norm_bwd_wide_cols_kernel<T>, cols, dim3(256), 0, st, y, x, mean, rstd, pg, pb,

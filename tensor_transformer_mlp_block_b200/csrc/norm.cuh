@@ -284,6 +284,260 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const T* dY, const T* __r
     }
 }
 
+// The 16 bytes of a vector as packed pairs of fp32.
+template <typename T>
+__device__ __forceinline__ void vec_pairs(const uint4& v, uint64_t* p) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            p[i] = f2_pack(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    } else {
+        p[0] = f2_pack(__uint_as_float(w[0]), __uint_as_float(w[1]));
+        p[1] = f2_pack(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    }
+}
+template <typename T>
+__device__ __forceinline__ uint4 pairs_vec(const uint64_t* p) {
+    uint32_t w[4];
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float a, b;
+            f2_unpack(p[i], a, b);
+            w[i] = pack_bf16x2(a, b);
+        }
+    } else {
+        float a, b;
+        f2_unpack(p[0], a, b);
+        w[0] = __float_as_uint(a);
+        w[1] = __float_as_uint(b);
+        f2_unpack(p[1], a, b);
+        w[2] = __float_as_uint(a);
+        w[3] = __float_as_uint(b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Backward of rows that are whole 16-byte vectors. As norm_bwd_kernel, but the
+// rows arrive through a shared-memory ring of bulk copies, so the bytes in
+// flight do not depend on the registers a thread can spare: a row's X, dY and
+// dR are one stage, read for the sums and again for dX (kept in registers in
+// between they would spill: the two weight gradients' sums take two registers
+// per element). A group of threads (a warp, or the block) owns a ring and walks
+// the rows group, group + groups, ...; a row's stage is refilled after the next
+// row's sums, whose barrier tells that every thread is through with it. Waits
+// are bounded.
+struct NormRing {
+    int stages;  // rows a group's ring holds (2..8)
+    uint64_t wait_limit_ns;
+};
+
+template <typename T, int NV, bool WARP, int MAX_THREADS>
+__global__ void __launch_bounds__(MAX_THREADS) norm_bwd_ring_kernel(const T* dY, const T* __restrict__ X,
+                                                            const T* __restrict__ gamma,
+                                                            const float* __restrict__ mean,
+                                                            const float* __restrict__ rstd, const T* dR, T* dX,
+                                                            float* __restrict__ part_g,
+                                                            float* __restrict__ part_b, int64_t R, int h,
+                                                            NormRing ring) {
+    constexpr int VE = 16 / sizeof(T), PV = VE / 2;
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ float red[2][2][32];
+    __shared__ __align__(8) uint64_t bars[4 * 8];
+    __shared__ int abort_flag;
+    const int nvec = h / VE;
+    const uint32_t row_bytes = static_cast<uint32_t>(h) * sizeof(T);
+    const uint32_t stage_bytes = row_bytes * (dR != nullptr ? 3 : 2);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int groups = WARP ? static_cast<int>(blockDim.y) : 1;
+    const int gi = WARP ? static_cast<int>(threadIdx.y) : 0;
+    const int S = ring.stages;
+    uint64_t* full = bars + gi * 8;
+    uint8_t* base = sm + static_cast<size_t>(gi) * S * stage_bytes;
+    volatile int* abort = &abort_flag;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) mbar_init(smem_u32(&full[s]), 1);
+        if (gi == 0) *abort = 0;
+        fence_mbar_init();
+    }
+    __syncthreads();
+    grid_dep_wait();
+    grid_dep_launch();
+
+    const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * groups + gi;
+    auto issue = [&](int64_t row, int s) {  // one thread: a row into stage s
+        const int64_t off = row * h;
+        const uint32_t bar = smem_u32(&full[s]), dst = smem_u32(base + s * stage_bytes);
+        mbar_arrive_expect_tx(bar, stage_bytes);
+        bulk_load(dst, X + off, row_bytes, bar);
+        bulk_load(dst + row_bytes, dY + off, row_bytes, bar);
+        if (dR != nullptr) bulk_load(dst + 2 * row_bytes, dR + off, row_bytes, bar);
+    };
+    if (threadIdx.x == 0)
+        for (int s = 0; s < S && first + s * step < R; ++s) issue(first + s * step, s);
+
+    const float inv_h = 1.0f / static_cast<float>(h);
+    // gamma behind the rings
+    uint4* sg = reinterpret_cast<uint4*>(sm + static_cast<size_t>(groups) * S * stage_bytes);
+    if (gamma != nullptr) {
+        const int n = blockDim.x * blockDim.y;
+        for (int v = threadIdx.y * blockDim.x + threadIdx.x; v < nvec; v += n)
+            sg[v] = *reinterpret_cast<const uint4*>(gamma + v * VE);
+        __syncthreads();
+    }
+    uint64_t ag[NV][PV], ab[NV][PV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < PV; ++e) ag[i][e] = ab[i][e] = 0ull;
+    float mu_next = first < R ? mean[first] : 0.0f, rs_next = first < R ? rstd[first] : 0.0f;
+    bool failed = false;
+    int at = 0, turn = 0;  // the row's stage, and its phase
+    uint32_t phase = 0;
+    int64_t r = first;
+    for (; r < R; r += step) {
+        const float mu = mu_next, rs = rs_next;
+        if (r + step < R) {
+            mu_next = mean[r + step];
+            rs_next = rstd[r + step];
+        }
+        const uint8_t* stage = base + at * stage_bytes;
+        const uint4* sx = reinterpret_cast<const uint4*>(stage);
+        const uint4* sy = reinterpret_cast<const uint4*>(stage + row_bytes);
+        const uint4* sr = reinterpret_cast<const uint4*>(stage + 2 * row_bytes);
+        const bool got = mbar_wait_bounded(smem_u32(&full[at]), phase, abort, ring.wait_limit_ns);
+        const uint64_t rs2 = f2_splat(rs), shift = f2_splat(-mu * rs);
+        uint64_t s1 = 0ull, s2 = 0ull;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = threadIdx.x + i * blockDim.x;
+            if (v >= nvec) continue;
+            uint64_t x[PV], y[PV], g[PV];
+            vec_pairs<T>(sx[v], x);
+            vec_pairs<T>(sy[v], y);
+            if (gamma != nullptr) vec_pairs<T>(sg[v], g);
+#pragma unroll
+            for (int e = 0; e < PV; ++e) {
+                const uint64_t xh = f2_fma(x[e], rs2, shift);
+                const uint64_t gy = gamma != nullptr ? f2_mul(y[e], g[e]) : y[e];
+                s1 = f2_add(s1, gy);
+                s2 = f2_fma(gy, xh, s2);
+                ag[i][e] = f2_fma(y[e], xh, ag[i][e]);
+                ab[i][e] = f2_add(ab[i][e], y[e]);
+            }
+        }
+        float c1, c2, hi;
+        f2_unpack(s1, c1, hi);
+        c1 = warp_sum(c1 + hi);
+        f2_unpack(s2, c2, hi);
+        c2 = warp_sum(c2 + hi);
+        if constexpr (WARP) {
+            failed = !__all_sync(0xffffffffu, got);
+        } else {
+            if (lane == 0) {
+                red[turn][0][warp] = c1;
+                red[turn][1][warp] = c2;
+            }
+            failed = __syncthreads_or(!got) != 0;
+            const bool in = lane < static_cast<int>(blockDim.x >> 5);
+            c1 = warp_sum(in ? red[turn][0][lane] : 0.0f);
+            c2 = warp_sum(in ? red[turn][1][lane] : 0.0f);
+            turn ^= 1;
+        }
+        if (failed) break;
+        // every thread is through with the previous row's stage: S - 1 rows on
+        if (threadIdx.x == 0 && r > first && r + (S - 1) * step < R)
+            issue(r + (S - 1) * step, at == 0 ? S - 1 : at - 1);
+        const uint64_t k1 = f2_splat(-rs * (c1 * inv_h)), k2 = f2_splat(-rs * (c2 * inv_h));
+        T* out = dX + r * h;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = threadIdx.x + i * blockDim.x;
+            if (v >= nvec) continue;
+            uint64_t x[PV], y[PV], g[PV], d[PV];
+            vec_pairs<T>(sx[v], x);
+            vec_pairs<T>(sy[v], y);
+            if (gamma != nullptr) vec_pairs<T>(sg[v], g);
+            if (dR != nullptr) vec_pairs<T>(sr[v], d);
+#pragma unroll
+            for (int e = 0; e < PV; ++e) {
+                const uint64_t xh = f2_fma(x[e], rs2, shift);
+                const uint64_t gy = gamma != nullptr ? f2_mul(y[e], g[e]) : y[e];
+                uint64_t o = f2_fma(xh, k2, f2_fma(gy, rs2, k1));
+                if (dR != nullptr) o = f2_add(o, d[e]);
+                x[e] = o;
+            }
+            *reinterpret_cast<uint4*>(out + v * VE) = pairs_vec<T>(x);
+        }
+        if (++at == S) {
+            at = 0;
+            phase ^= 1u;
+        }
+    }
+    if (failed) {
+        if (lane == 0) raise_timeout(abort);
+        if (threadIdx.x == 0) {
+            // wind down: the copies still in flight, from this row's on (the
+            // previous row's stage has not been filled again)
+            for (int q = 0; q < (r == first ? S : S - 1) && r + q * step < R; ++q) {
+                volatile int never = 0;
+                mbar_wait_bounded(smem_u32(&full[at]), phase, &never, ring.wait_limit_ns);
+                if (++at == S) {
+                    at = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    }
+    if constexpr (!WARP) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int v = threadIdx.x + i * blockDim.x;
+            if (v >= nvec) continue;
+            float4* pg = reinterpret_cast<float4*>(part_g + static_cast<int64_t>(blockIdx.x) * h + v * VE);
+            float4* pb = reinterpret_cast<float4*>(part_b + static_cast<int64_t>(blockIdx.x) * h + v * VE);
+#pragma unroll
+            for (int e = 0; e < PV; e += 2) {
+                float4 a;
+                f2_unpack(ag[i][e], a.x, a.y);
+                f2_unpack(ag[i][e + 1], a.z, a.w);
+                pg[e / 2] = a;
+                f2_unpack(ab[i][e], a.x, a.y);
+                f2_unpack(ab[i][e + 1], a.z, a.w);
+                pb[e / 2] = a;
+            }
+        }
+    } else {
+        // the block's warps in order, through the ring's memory: dgamma's sums,
+        // then dbeta's (the host leaves room for groups × h floats)
+        float* fold = reinterpret_cast<float*>(sm);
+        for (int which = 0; which < 2; ++which) {
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int v = threadIdx.x + i * blockDim.x;
+                if (v >= nvec) continue;
+                float2* f = reinterpret_cast<float2*>(fold + gi * h + v * VE);
+#pragma unroll
+                for (int e = 0; e < PV; ++e) {
+                    float a, b;
+                    f2_unpack(which == 0 ? ag[i][e] : ab[i][e], a, b);
+                    f[e] = make_float2(a, b);
+                }
+            }
+            __syncthreads();
+            float* out = (which == 0 ? part_g : part_b) + static_cast<int64_t>(blockIdx.x) * h;
+            for (int c = gi * 32 + lane; c < h; c += 32 * groups) {
+                float s = fold[c];
+                for (int y = 1; y < groups; ++y) s += fold[y * h + c];
+                out[c] = s;
+            }
+        }
+    }
+}
+
 // Rows too wide for registers: one block of 1024 threads per row, X read three
 // times (from L2 after the first), one element per access.
 template <typename T>
