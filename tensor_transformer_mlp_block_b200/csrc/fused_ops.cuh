@@ -67,69 +67,93 @@ SimtArgs plain_args(int64_t M, int64_t N, int64_t K, const void* A, int64_t sam,
 
 // ------------------------------------------------------------------ layer norm
 
-// Shape of a norm kernel's blocks: VE elements per access, `elems` elements
-// per thread, `threads` per row, `rows` rows per block. threads = 0: the row
-// does not fit the registers (looped kernels).
+// Shape of a norm kernel's blocks: `elems` elements per thread, `threads` per
+// row, `rows` rows per block. threads = 0: the row does not fit the registers
+// (looped kernels).
 struct NormShape {
-    int ve, elems, threads, rows;
+    int elems, threads, rows;
 };
 
 constexpr int kNormRows = 4;  // rows per block with one warp per row
 
-NormShape norm_shape(int64_t h, int esize, bool vec, bool back) {
-    const int ve = vec ? 16 / esize : 1;
-    const int64_t nvec = h / ve;
-    if (h <= 1024) {  // one warp per row
+// Forward. With few rows (no more than two per SM) latency counts: as many
+// threads per row as there are. Else 64 bytes or more per thread keep enough
+// of memory in flight. Measured on B200, µs at 8 / 16 / 32 elements: 1 row of
+// 4096 bf16 2.6 / 3.1 / 3.6; 8192 rows 51 / 41 / 32 (fp32 50 / 46 / 44). Rows up
+// to 1024 go to a warp each (1024 columns: 15.4 against 20-23 µs at 16384
+// rows). Single elements do best with 8 per thread (4099 columns: 72 / 82 / 114).
+NormShape norm_shape(int64_t T, int64_t h, bool vec) {
+    auto fit = [&](int e, int most) {
+        const int64_t t = ((h + e - 1) / e + 31) / 32 * 32;
+        return t <= most ? static_cast<int>(t) : 0;
+    };
+    const bool few = T <= 2 * static_cast<int64_t>(plan_num_sms());
+    if (vec && !few && h <= 1024) {
         for (int e : {8, 16, 32})
-            if (h <= 32 * e) return {ve, e, 32, kNormRows};
+            if (h <= 32 * e) return {e, 32, kNormRows};
     }
-    const int limit[3] = {256, 512, back ? 512 : 1024};
-    const int el[3] = {8, 16, 32};
-    for (int i = 0; i < 3; ++i) {
-        const int nv = el[i] / ve;
-        const int64_t t = ((nvec + nv - 1) / nv + 31) / 32 * 32;
-        if (t <= limit[i]) return {ve, el[i], static_cast<int>(t), 1};
+    if (vec && !few && fit(32, 1024) > 0) return {32, fit(32, 1024), 1};
+    for (int e : {8, 16, 32}) {
+        const int t = fit(e, 1024);
+        if (t > 0) return {e, t, t == 32 ? kNormRows : 1};
     }
-    return {1, 0, 0, 1};
+    return {0, 0, 1};
 }
 
-// Blocks of the backward kernel (each leaves one partial row of dgamma and
-// dbeta): about 1024 threads per SM.
+// Shape of the backward kernel of rows that are not whole vectors
+// (norm_bwd_kernel): 8 columns per thread up to 4096, else 16 (up to 128
+// registers a thread). threads = 0: wider rows (looped kernels).
+NormShape norm_scalar_shape(int64_t h) {
+    const int e = h <= 8 * 512 ? 8 : 16;
+    const int64_t t = ((h + e - 1) / e + 31) / 32 * 32;
+    return NormShape{e, t <= 512 ? static_cast<int>(t) : 0, 1};
+}
+
+// Its blocks (each leaves one partial row of dgamma and dbeta).
 int64_t norm_bwd_blocks(int64_t T, const NormShape& s) {
-    if (s.threads == 0) return std::min<int64_t>((T + 127) / 128, 1024);
-    const int64_t per_sm = std::max(1, 1024 / (s.threads * s.rows));
-    return std::max<int64_t>(1, std::min((T + s.rows - 1) / s.rows, plan_num_sms() * per_sm));
+    if (s.threads == 0) return std::max<int64_t>(1, std::min<int64_t>((T + 127) / 128, 1024));
+    return std::max<int64_t>(1, std::min<int64_t>(T, int64_t(plan_num_sms()) * std::min(16, std::max(1, 768 / s.threads))));
 }
 
 // Shape of the ring kernel (norm_bwd_ring_kernel) for rows of whole 16-byte
 // vectors: `elems` elements per thread, `threads` per row, `rows` groups per
 // block, `per_sm` blocks per SM, a ring of `stages` rows per group. threads =
-// 0: two rows of X, dY and dR do not fit a block's shared memory.
+// 0: not even one row of X, dY and dR fits a block's shared memory, or the row
+// has more than 512 × 32 elements.
+// The table is measured (B200, µs at 128 Mi elements or less, bf16): a warp per
+// row up to 512 columns (512: 32 against 43 with blocks); 16 columns per thread
+// from there (1024: 35 against 38 with 8 per thread and 79 with a warp per row
+// and 32; 4096: 51.5 against 60 and 74), as many blocks as 64 K registers hold.
 struct NormRingShape {
     int elems, threads, rows, per_sm, stages;
+    bool gamma_shared;
 };
 
-constexpr int kNormRingBytes = 224 * 1024;  // of shared memory per SM, for all blocks
+// Dynamic shared memory of one block with `per_sm` resident: of 228 KB per SM
+// a block costs 1 KB, may have 227 KB, and the kernel's static part needs 2 KB.
+int64_t norm_ring_room(int per_sm) { return std::min(227, 228 / per_sm - 1) * int64_t(1024) - 2048; }
 
 NormRingShape norm_ring_shape(int64_t h, int esize) {
-    NormRingShape s{0, 0, 1, 1, 0};
-    const int64_t stage = 3 * h * esize, gamma = h * esize, other = 2048;  // bytes
-    if (h <= 1024) {  // a warp per row
-        s.elems = h <= 256 ? 8 : h <= 512 ? 16 : 32;
+    const NormRingShape none{0, 0, 1, 1, 0, false};
+    NormRingShape s = none;
+    const int64_t stage = 3 * h * esize, gamma = h * esize;
+    if (h <= 512) {  // a warp per row
+        s.elems = h <= 256 ? 8 : 16;
         s.threads = 32;
         s.rows = kNormRows;
         s.per_sm = 4;
     } else {
-        s.elems = h <= 16 * 768 ? 16 : 32;
+        s.elems = h <= 16 * 768 && (esize == 2 || 2 * stage + gamma <= norm_ring_room(1)) ? 16 : 32;
         const int64_t t = ((h + s.elems - 1) / s.elems + 31) / 32 * 32;
-        if (t > (s.elems == 16 ? 768 : 512)) return NormRingShape{0, 0, 1, 1, 0};
+        if (t > (s.elems == 16 ? 768 : 512)) return none;
         s.threads = static_cast<int>(t);
-        s.per_sm = t <= 128 ? 4 : t <= 256 ? 2 : 1;
+        s.per_sm = t <= 64 ? 8 : t <= 128 ? 4 : t <= 256 ? 2 : 1;
     }
-    auto fit = [&] { return (kNormRingBytes / s.per_sm - gamma - other) / (stage * s.rows); };
+    auto fit = [&] { return (norm_ring_room(s.per_sm) - gamma) / (stage * s.rows); };
     while (s.per_sm > 1 && fit() < 3) --s.per_sm;
-    if (fit() < 2) return NormRingShape{0, 0, 1, 1, 0};
-    s.stages = static_cast<int>(std::min<int64_t>(fit(), 4));
+    s.gamma_shared = fit() >= 2;
+    s.stages = static_cast<int>(s.gamma_shared ? std::min<int64_t>(fit(), 4) : 1);
+    if (!s.gamma_shared && (stage > norm_ring_room(1) || s.elems != 32)) return none;
     return s;
 }
 
@@ -139,141 +163,87 @@ int64_t norm_ring_blocks(int64_t T, const NormRingShape& s) {
 
 size_t norm_workspace(int64_t T, int64_t h, tpmlp_dtype dt) {
     const int esize = dt == TPMLP_BF16 ? 2 : 4;
-    int64_t blocks = norm_bwd_blocks(T, norm_shape(h, esize, false, true));
+    int64_t blocks = norm_bwd_blocks(T, norm_scalar_shape(h));
     if (h % (16 / esize) == 0) {
-        blocks = std::max(blocks, norm_bwd_blocks(T, norm_shape(h, esize, true, true)));
         const NormRingShape ring = norm_ring_shape(h, esize);
         if (ring.threads > 0) blocks = std::max(blocks, norm_ring_blocks(T, ring));
     }
     return 2 * round256(static_cast<size_t>(blocks) * h * sizeof(float));
 }
 
-// Lets `kern` use up to kNormRingBytes of dynamic shared memory (once per device).
+// Lets `kern` use any dynamic shared memory that norm_ring_shape asks for
+// (once per device).
 template <auto KERNEL>
 tpmlp_status allow_ring_smem() {
     static std::atomic<bool> set[kMaxDevices] = {};
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TPMLP_ERR_CUDA;
     if (!set[dev].load()) {
-        if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRingBytes) != cudaSuccess)
+        if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(norm_ring_room(1))) != cudaSuccess)
             return TPMLP_ERR_CUDA;
         set[dev].store(true);
     }
     return TPMLP_OK;
 }
 
-template <typename T, int NV, bool WARP, int MAX_THREADS>
+template <typename T, int NV, bool WARP, int MAX_THREADS, int PER_SM, bool KEEP, bool ONE = false>
 tpmlp_status norm_ring_launch(const NormRingShape& s, const T* dY, const T* X, const T* gamma, const float* mean,
                               const float* rstd, const T* dR, T* dX, float* pg, float* pb, int64_t blocks, int64_t R,
                               int64_t h, cudaStream_t st) {
-    TPMLP_TRY((allow_ring_smem<norm_bwd_ring_kernel<T, NV, WARP, MAX_THREADS>>()));
+    TPMLP_TRY((allow_ring_smem<norm_bwd_ring_kernel<T, NV, WARP, MAX_THREADS, PER_SM, KEEP, ONE>>()));
     // the rings, and gamma behind them
-    const size_t smem = (static_cast<size_t>(s.rows) * s.stages * (dR != nullptr ? 3 : 2) + 1) * h * sizeof(T);
-    return launch_dep(norm_bwd_ring_kernel<T, NV, WARP, MAX_THREADS>, dim3(static_cast<unsigned>(blocks)), dim3(s.threads, s.rows),
-                      smem, st, dY, X, gamma, mean, rstd, dR, dX, pg, pb, R, static_cast<int>(h),
+    const size_t smem = (static_cast<size_t>(s.rows) * s.stages * (dR != nullptr ? 3 : 2) + (s.gamma_shared ? 1 : 0)) *
+                        h * sizeof(T);
+    return launch_dep(norm_bwd_ring_kernel<T, NV, WARP, MAX_THREADS, PER_SM, KEEP, ONE>,
+                      dim3(static_cast<unsigned>(blocks)), dim3(s.threads, s.rows), smem, st, dY, X, gamma, mean,
+                      rstd, dR, dX, pg, pb, R, static_cast<int>(h),
                       NormRing{s.stages, g_wait_limit_ns.load()});
 }
 
-template <typename T, bool WARP>
-tpmlp_status norm_ring_dispatch(const NormRingShape& s, const T* dY, const T* X, const T* gamma, const float* mean,
-                                const float* rstd, const T* dR, T* dX, float* pg, float* pb, int64_t blocks,
-                                int64_t R, int64_t h, cudaStream_t st) {
+template <typename T>
+tpmlp_status norm_ring(const NormRingShape& s, const T* dY, const T* X, const T* gamma, const float* mean,
+                       const float* rstd, const T* dR, T* dX, float* pg, float* pb, int64_t blocks, int64_t R,
+                       int64_t h, cudaStream_t st) {
     constexpr int kVec = 16 / sizeof(T);
-#define TPMLP_RING(NV, MAX) \
-    norm_ring_launch<T, NV, WARP, MAX>(s, dY, X, gamma, mean, rstd, dR, dX, pg, pb, blocks, R, h, st)
-    if constexpr (WARP) {
-        if (s.elems == 8) return TPMLP_RING(8 / kVec, 32 * kNormRows);
-        if (s.elems == 16) return TPMLP_RING(16 / kVec, 32 * kNormRows);
-        return TPMLP_RING(32 / kVec, 32 * kNormRows);
-    } else {
-        // 512 threads may take 128 registers each, 768 only 80
-        if (s.elems == 16) return s.threads <= 512 ? TPMLP_RING(16 / kVec, 512) : TPMLP_RING(16 / kVec, 768);
-        return TPMLP_RING(32 / kVec, 512);
+#define TPMLP_RING(NV, ...) \
+    norm_ring_launch<T, NV, __VA_ARGS__>(s, dY, X, gamma, mean, rstd, dR, dX, pg, pb, blocks, R, h, st)
+    if (s.threads == 32)
+        return s.elems == 8 ? TPMLP_RING(8 / kVec, true, 32 * kNormRows, 4, true)
+                            : TPMLP_RING(16 / kVec, true, 32 * kNormRows, 4, true);
+    if (s.elems == 16) {
+        // registers a thread: 128 up to 512 threads per SM, 80 at 768
+        if (s.threads <= 256) return TPMLP_RING(16 / kVec, false, 256, 2, true);
+        return s.threads <= 512 ? TPMLP_RING(16 / kVec, false, 512, 1, true)
+                                : TPMLP_RING(16 / kVec, false, 768, 1, false);
     }
+    return s.gamma_shared ? TPMLP_RING(32 / kVec, false, 512, 1, false)
+                          : TPMLP_RING(32 / kVec, false, 512, 1, false, true);
 #undef TPMLP_RING
 }
 
-template <typename T, int VE, int NV>
-tpmlp_status norm_fwd_launch(const NormShape& s, const T* X, const T* gamma, const T* beta, T* Y, float* mean,
-                             float* rstd, int64_t R, int64_t h, float eps, cudaStream_t st) {
-    const dim3 grid(static_cast<unsigned>((R + s.rows - 1) / s.rows)), block(s.threads, s.rows);
-    return launch_dep(norm_fwd_kernel<T, VE, NV>, grid, block, 0, st, X, gamma, beta, Y, mean, rstd, R,
-                      static_cast<int>(h), eps);
-}
-
-template <typename T, int VE, int NV>
-tpmlp_status norm_bwd_launch(const NormShape& s, const T* dY, const T* X, const T* gamma, const float* mean,
-                             const float* rstd, const T* dR, T* dX, float* pg, float* pb, int64_t blocks,
-                             int64_t R, int64_t h, cudaStream_t st) {
-    const size_t fold = s.rows > 1 ? static_cast<size_t>(s.rows) * h * sizeof(float) : 0;
-    return launch_dep(norm_bwd_kernel<T, VE, NV>, dim3(static_cast<unsigned>(blocks)), dim3(s.threads, s.rows),
-                      fold, st, dY, X, gamma, mean, rstd, dR, dX, pg, pb, R, static_cast<int>(h));
-}
-
-// Calls f.template operator()<VE, NV>() for the shape's vector width and count.
-template <typename T, class F>
-tpmlp_status norm_dispatch(const NormShape& s, F&& f) {
-    constexpr int kVec = 16 / sizeof(T);
-    if (s.ve == 1) {
-        switch (s.elems) {
-            case 8: return f.template operator()<1, 8>();
-            case 16: return f.template operator()<1, 16>();
-            default: return f.template operator()<1, 32>();
-        }
-    }
-    switch (s.elems) {
-        case 8: return f.template operator()<kVec, 8 / kVec>();
-        case 16: return f.template operator()<kVec, 16 / kVec>();
-        default: return f.template operator()<kVec, 32 / kVec>();
-    }
-}
-
 template <typename T>
-struct NormFwdCall {
-    NormShape s;
-    const T *X, *gamma, *beta;
-    T* Y;
-    float *mean, *rstd;
-    int64_t R, h;
-    float eps;
-    cudaStream_t st;
-    template <int VE, int NV>
-    tpmlp_status operator()() const {
-        return norm_fwd_launch<T, VE, NV>(s, X, gamma, beta, Y, mean, rstd, R, h, eps, st);
-    }
-};
-
-template <typename T>
-struct NormBwdCall {
-    NormShape s;
-    const T *dY, *X, *gamma;
-    const float *mean, *rstd;
-    const T* dR;
-    T* dX;
-    float *pg, *pb;
-    int64_t blocks, R, h;
-    cudaStream_t st;
-    template <int VE, int NV>
-    tpmlp_status operator()() const {
-        return norm_bwd_launch<T, VE, NV>(s, dY, X, gamma, mean, rstd, dR, dX, pg, pb, blocks, R, h, st);
-    }
-};
-
-template <typename T>
-tpmlp_status norm_fwd_impl(const void* X, const void* gamma, const void* beta, void* Y, float* mean,
+tpmlp_status norm_fwd_impl(const void* X_, const void* gamma_, const void* beta_, void* Y_, float* mean,
                            float* rstd, int64_t R, int64_t h, float eps, cudaStream_t st) {
-    const bool vec = h % (16 / sizeof(T)) == 0 && aligned16(X) && aligned16(Y) && aligned16(gamma) &&
-                     aligned16(beta);
-    const NormShape s = norm_shape(h, sizeof(T), vec, false);
-    const double bytes = sizeof(T) * (2.0 * R * h + 2.0 * h) + 8.0 * R;
-    return timed(K_N_FWD, 0.0, bytes, st, [&] {
+    constexpr int kVec = 16 / sizeof(T);
+    const bool vec = h % kVec == 0 && aligned16(X_) && aligned16(Y_) && aligned16(gamma_) && aligned16(beta_);
+    const NormShape s = norm_shape(R, h, vec);
+    const T *X = static_cast<const T*>(X_), *gamma = static_cast<const T*>(gamma_),
+            *beta = static_cast<const T*>(beta_);
+    T* Y = static_cast<T*>(Y_);
+    return timed(K_N_FWD, 0.0, sizeof(T) * (2.0 * R * h + 2.0 * h) + 8.0 * R, st, [&] {
         if (s.threads == 0)
-            return launch_dep(norm_fwd_wide_kernel<T>, dim3(static_cast<unsigned>(R)), dim3(1024), 0, st,
-                              static_cast<const T*>(X), static_cast<const T*>(gamma),
-                              static_cast<const T*>(beta), static_cast<T*>(Y), mean, rstd, h, eps);
-        return norm_dispatch<T>(s, NormFwdCall<T>{s, static_cast<const T*>(X), static_cast<const T*>(gamma),
-                                                  static_cast<const T*>(beta), static_cast<T*>(Y), mean, rstd,
-                                                  R, h, eps, st});
+            return launch_dep(norm_fwd_wide_kernel<T>, dim3(static_cast<unsigned>(R)), dim3(1024), 0, st, X, gamma,
+                              beta, Y, mean, rstd, h, eps);
+        const dim3 grid(static_cast<unsigned>((R + s.rows - 1) / s.rows)), block(s.threads, s.rows);
+        auto kern = vec ? (s.elems == 8    ? norm_fwd_kernel<T, 8 / kVec>
+                           : s.elems == 16 ? norm_fwd_kernel<T, 16 / kVec>
+                                           : norm_fwd_kernel<T, 32 / kVec>)
+                        : (s.elems == 8    ? norm_fwd_scalar_kernel<T, 8>
+                           : s.elems == 16 ? norm_fwd_scalar_kernel<T, 16>
+                                           : norm_fwd_scalar_kernel<T, 32>);
+        return launch_dep(kern, grid, block, 0, st, X, gamma, beta, Y, mean, rstd, R, static_cast<int>(h),
+                          1.0f / static_cast<float>(h), eps);
     });
 }
 
@@ -283,8 +253,8 @@ tpmlp_status norm_bwd_impl(const void* dY, const void* X, const void* gamma, con
                            int64_t h, void* workspace, cudaStream_t st) {
     const bool vec = h % (16 / sizeof(T)) == 0 && aligned16(dY) && aligned16(X) && aligned16(gamma) &&
                      aligned16(dR) && aligned16(dX);
-    const NormShape s = norm_shape(h, sizeof(T), vec, true);
-    const NormRingShape ring = vec ? norm_ring_shape(h, sizeof(T)) : NormRingShape{0, 0, 1, 1, 0};
+    const NormShape s = norm_scalar_shape(h);
+    const NormRingShape ring = vec ? norm_ring_shape(h, sizeof(T)) : NormRingShape{0, 0, 1, 1, 0, false};
     const int64_t blocks = ring.threads > 0 ? norm_ring_blocks(R, ring) : norm_bwd_blocks(R, s);
     float* pg = static_cast<float*>(workspace);
     float* pb = reinterpret_cast<float*>(static_cast<char*>(workspace) +
@@ -296,10 +266,7 @@ tpmlp_status norm_bwd_impl(const void* dY, const void* X, const void* gamma, con
     T* dx = static_cast<T*>(dX);
     const double bytes = sizeof(T) * ((dR ? 4.0 : 3.0) * R * h + h) + 8.0 * R + 8.0 * blocks * h;
     TPMLP_TRY(timed(K_N_BWD, 0.0, bytes, st, [&]() -> tpmlp_status {
-        if (ring.threads == 32)
-            return norm_ring_dispatch<T, true>(ring, y, x, g, mean, rstd, d, dx, pg, pb, blocks, R, h, st);
-        if (ring.threads > 0)
-            return norm_ring_dispatch<T, false>(ring, y, x, g, mean, rstd, d, dx, pg, pb, blocks, R, h, st);
+        if (ring.threads > 0) return norm_ring<T>(ring, y, x, g, mean, rstd, d, dx, pg, pb, blocks, R, h, st);
         if (s.threads == 0) {
             const dim3 cols(static_cast<unsigned>(blocks), static_cast<unsigned>((h + 255) / 256));
             TPMLP_TRY(launch_dep(norm_bwd_wide_cols_kernel<T>, cols, dim3(256), 0, st, y, x, mean, rstd, pg, pb,
@@ -307,7 +274,12 @@ tpmlp_status norm_bwd_impl(const void* dY, const void* X, const void* gamma, con
             return launch_dep(norm_bwd_wide_kernel<T>, dim3(static_cast<unsigned>(R)), dim3(1024), 0, st, y, x,
                               g, mean, rstd, d, dx, h);
         }
-        return norm_dispatch<T>(s, NormBwdCall<T>{s, y, x, g, mean, rstd, d, dx, pg, pb, blocks, R, h, st});
+        const dim3 grid(static_cast<unsigned>(blocks)), block(s.threads);
+        if (s.elems == 8)
+            return launch_dep(norm_bwd_kernel<T, 8>, grid, block, 0, st, y, x, g, mean, rstd, d, dx, pg, pb, R,
+                              static_cast<int>(h));
+        return launch_dep(norm_bwd_kernel<T, 16>, grid, block, 0, st, y, x, g, mean, rstd, d, dx, pg, pb, R,
+                          static_cast<int>(h));
     }));
     return colsum_finish2(K_N_DGB, pg, blocks, h, dgamma, pb, blocks, h, dbeta, st);
 }

@@ -13,45 +13,6 @@
 
 namespace tpmlp {
 
-// VE elements of a row as they lie in memory: 16 bytes, or one element.
-template <typename T, int VE>
-struct RawVec {
-    uint4 v;
-    __device__ __forceinline__ void load(const T* p) { v = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void clear() { v = make_uint4(0, 0, 0, 0); }
-    __device__ __forceinline__ void get(float* f) const {
-        if constexpr (sizeof(T) == 2) {
-            unpack_bf16x8(v, f);
-        } else {
-            f[0] = __uint_as_float(v.x);
-            f[1] = __uint_as_float(v.y);
-            f[2] = __uint_as_float(v.z);
-            f[3] = __uint_as_float(v.w);
-        }
-    }
-    __device__ __forceinline__ static void store(T* p, const float* f) {
-        uint4 o;
-        if constexpr (sizeof(T) == 2) {
-            o.x = pack_bf16x2(f[0], f[1]);
-            o.y = pack_bf16x2(f[2], f[3]);
-            o.z = pack_bf16x2(f[4], f[5]);
-            o.w = pack_bf16x2(f[6], f[7]);
-        } else {
-            o = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                           __float_as_uint(f[3]));
-        }
-        *reinterpret_cast<uint4*>(p) = o;
-    }
-};
-template <typename T>
-struct RawVec<T, 1> {
-    T v;
-    __device__ __forceinline__ void load(const T* p) { v = *p; }
-    __device__ __forceinline__ void clear() { v = from_f32<T>(0.0f); }
-    __device__ __forceinline__ void get(float* f) const { f[0] = to_f32<T>(v); }
-    __device__ __forceinline__ static void store(T* p, const float* f) { *p = from_f32<T>(f[0]); }
-};
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int w = 16; w >= 1; w >>= 1) v += __shfl_xor_sync(0xffffffffu, v, w);
@@ -68,220 +29,6 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
     if (lane == 0) red[warp] = v;
     __syncthreads();
     return warp_sum(lane < static_cast<int>(blockDim.x >> 5) ? red[lane] : 0.0f);
-}
-
-// Block (threads per row, rows): with 32 threads per row the rows of a block
-// are independent warps; else one row per block. Thread t holds the vectors
-// t, t + threads, ... of the row.
-template <typename T, int VE, int NV>
-__global__ void __launch_bounds__(1024) norm_fwd_kernel(const T* __restrict__ X, const T* __restrict__ gamma,
-                                                       const T* __restrict__ beta, T* __restrict__ Y,
-                                                       float* __restrict__ mean, float* __restrict__ rstd,
-                                                       int64_t R, int h, float eps) {
-    __shared__ float red[2][32];
-    grid_dep_wait();
-    grid_dep_launch();
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-    if (r >= R) return;  // a whole warp of a 32-thread row; never with one row per block
-    const int nvec = h / VE;
-    const T* x = X + r * h;
-    RawVec<T, VE> raw[NV];
-    float f[NV][VE];
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        raw[i].clear();
-        if (v < nvec) raw[i].load(x + v * VE);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        raw[i].get(f[i]);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) s += f[i][e];
-    }
-    const float inv_h = 1.0f / static_cast<float>(h);
-    const float mu = row_sum(s, red[0]) * inv_h;
-    float q = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        if (static_cast<int>(threadIdx.x + i * blockDim.x) < nvec) {
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const float c = f[i][e] - mu;
-                q += c * c;
-            }
-        }
-    }
-    const float rs = 1.0f / sqrtf(row_sum(q, red[1]) * inv_h + eps);
-    if (threadIdx.x == 0 && mean != nullptr) {
-        mean[r] = mu;
-        rstd[r] = rs;
-    }
-    T* y = Y + r * h;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        if (v < nvec) {
-            float o[VE];
-            RawVec<T, VE> g, b;
-            float gf[VE], bf[VE];
-            if (gamma != nullptr) {
-                g.load(gamma + v * VE);
-                g.get(gf);
-            }
-            if (beta != nullptr) {
-                b.load(beta + v * VE);
-                b.get(bf);
-            }
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                o[e] = (f[i][e] - mu) * rs;
-                if (gamma != nullptr) o[e] *= gf[e];
-                if (beta != nullptr) o[e] += bf[e];
-            }
-            RawVec<T, VE>::store(y + v * VE, o);
-        }
-    }
-}
-
-// Backward. Blocks walk the rows r = block, block + grid, ...; a thread owns
-// the same columns in every row and keeps their dgamma and dbeta sums in
-// registers, so the weight gradients cost no second pass over the data: each
-// block writes one row of partial sums, which colsum_final2_kernel adds in
-// block order. The next row's loads are issued before the current row's sums.
-template <typename T, int VE, int NV>
-__global__ void __launch_bounds__(512) norm_bwd_kernel(const T* dY, const T* __restrict__ X,
-                                                       const T* __restrict__ gamma,
-                                                       const float* __restrict__ mean,
-                                                       const float* __restrict__ rstd, const T* dR, T* dX,
-                                                       float* __restrict__ part_g, float* __restrict__ part_b,
-                                                       int64_t R, int h) {
-    extern __shared__ float fold[];  // rows of a block > 1: its groups' sums
-    __shared__ float red[2][2][32];
-    grid_dep_wait();
-    grid_dep_launch();
-    const int nvec = h / VE;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
-    const float inv_h = 1.0f / static_cast<float>(h);
-    RawVec<T, VE> rg[NV];
-    float ag[NV][VE], ab[NV][VE];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int v = threadIdx.x + i * blockDim.x;
-        rg[i].clear();
-        if (gamma != nullptr && v < nvec) rg[i].load(gamma + v * VE);
-#pragma unroll
-        for (int e = 0; e < VE; ++e) ag[i][e] = ab[i][e] = 0.0f;
-    }
-    int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-    int turn = 0;
-    for (; r < R; r += step) {
-        RawVec<T, VE> rx[NV], ry[NV];
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = threadIdx.x + i * blockDim.x;
-            rx[i].clear();
-            ry[i].clear();
-            if (v < nvec) {
-                rx[i].load(X + r * h + v * VE);
-                ry[i].load(dY + r * h + v * VE);
-            }
-        }
-        const float mu = mean[r], rs = rstd[r];
-        float c1 = 0.0f, c2 = 0.0f;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (static_cast<int>(threadIdx.x + i * blockDim.x) >= nvec) continue;
-            float x[VE], y[VE], g[VE];
-            rx[i].get(x);
-            ry[i].get(y);
-            rg[i].get(g);
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const float xh = (x[e] - mu) * rs;
-                const float gy = gamma != nullptr ? y[e] * g[e] : y[e];
-                c1 += gy;
-                c2 += gy * xh;
-                ag[i][e] += y[e] * xh;
-                ab[i][e] += y[e];
-            }
-        }
-        c1 = warp_sum(c1);
-        c2 = warp_sum(c2);
-        if (blockDim.x > 32) {
-            // two sets of slots in turn: one barrier per row
-            if (lane == 0) {
-                red[turn][0][warp] = c1;
-                red[turn][1][warp] = c2;
-            }
-            __syncthreads();
-            const bool in = lane < static_cast<int>(blockDim.x >> 5);
-            c1 = warp_sum(in ? red[turn][0][lane] : 0.0f);
-            c2 = warp_sum(in ? red[turn][1][lane] : 0.0f);
-            turn ^= 1;
-        }
-        c1 *= inv_h;
-        c2 *= inv_h;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = threadIdx.x + i * blockDim.x;
-            if (v >= nvec) continue;
-            float x[VE], y[VE], g[VE], o[VE];
-            rx[i].get(x);
-            ry[i].get(y);
-            rg[i].get(g);
-            float d[VE];
-            if (dR != nullptr) {
-                RawVec<T, VE> q;
-                q.load(dR + r * h + v * VE);
-                q.get(d);
-            }
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const float xh = (x[e] - mu) * rs;
-                const float gy = gamma != nullptr ? y[e] * g[e] : y[e];
-                o[e] = rs * (gy - c1 - xh * c2);
-                if (dR != nullptr) o[e] += d[e];
-            }
-            RawVec<T, VE>::store(dX + r * h + v * VE, o);
-        }
-    }
-    if (blockDim.y == 1) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = threadIdx.x + i * blockDim.x;
-            if (v < nvec) {
-#pragma unroll
-                for (int e = 0; e < VE; ++e) {
-                    part_g[static_cast<int64_t>(blockIdx.x) * h + v * VE + e] = ag[i][e];
-                    part_b[static_cast<int64_t>(blockIdx.x) * h + v * VE + e] = ab[i][e];
-                }
-            }
-        }
-        return;
-    }
-    // the block's rows in ascending order, dgamma's sums and then dbeta's
-    for (int which = 0; which < 2; ++which) {
-        __syncthreads();
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int v = threadIdx.x + i * blockDim.x;
-            if (v < nvec) {
-#pragma unroll
-                for (int e = 0; e < VE; ++e)
-                    fold[threadIdx.y * h + v * VE + e] = which == 0 ? ag[i][e] : ab[i][e];
-            }
-        }
-        __syncthreads();
-        float* out = (which == 0 ? part_g : part_b) + static_cast<int64_t>(blockIdx.x) * h;
-        for (int c = threadIdx.y * 32 + threadIdx.x; c < h; c += 32 * blockDim.y) {
-            float s = fold[c];
-            for (int y = 1; y < static_cast<int>(blockDim.y); ++y) s += fold[y * h + c];
-            out[c] = s;
-        }
-    }
 }
 
 // The 16 bytes of a vector as packed pairs of fp32.
@@ -319,22 +66,220 @@ __device__ __forceinline__ uint4 pairs_vec(const uint64_t* p) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Block (threads per row, rows): with 32 threads per row the rows of a block
+// are independent warps; else one row per block. Thread t holds the vectors
+// t, t + threads, ... of the row, as packed pairs of fp32.
+template <typename T, int NV>
+__global__ void __launch_bounds__(1024) norm_fwd_kernel(const T* __restrict__ X, const T* __restrict__ gamma,
+                                                       const T* __restrict__ beta, T* __restrict__ Y,
+                                                       float* __restrict__ mean, float* __restrict__ rstd,
+                                                       int64_t R, int h, float inv_h, float eps) {
+    constexpr int VE = 16 / sizeof(T), PV = VE / 2;
+    __shared__ float red[2][32];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (r >= R) return;  // a whole warp of a 32-thread row; never with one row per block
+    const int nvec = h / VE;
+    const uint4* x = reinterpret_cast<const uint4*>(X + r * h);
+    uint4 raw[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        raw[i] = v < nvec ? x[v] : make_uint4(0, 0, 0, 0);
+    }
+    uint64_t f[NV][PV];
+    uint64_t s = 0ull;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        vec_pairs<T>(raw[i], f[i]);
+#pragma unroll
+        for (int e = 0; e < PV; ++e) s = f2_add(s, f[i][e]);
+    }
+    float a, b;
+    f2_unpack(s, a, b);
+    const float mu = row_sum(a + b, red[0]) * inv_h;
+    const uint64_t less = f2_splat(-mu);
+    uint64_t q = 0ull;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        if (static_cast<int>(threadIdx.x + i * blockDim.x) >= nvec) continue;
+#pragma unroll
+        for (int e = 0; e < PV; ++e) {
+            f[i][e] = f2_add(f[i][e], less);
+            q = f2_fma(f[i][e], f[i][e], q);
+        }
+    }
+    f2_unpack(q, a, b);
+    const float rs = rsqrtf(row_sum(a + b, red[1]) * inv_h + eps);
+    if (threadIdx.x == 0 && mean != nullptr) {
+        mean[r] = mu;
+        rstd[r] = rs;
+    }
+    const uint64_t rs2 = f2_splat(rs);
+    uint4* y = reinterpret_cast<uint4*>(Y + r * h);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int v = threadIdx.x + i * blockDim.x;
+        if (v >= nvec) continue;
+        uint64_t g[PV], c[PV];
+        if (gamma != nullptr) vec_pairs<T>(reinterpret_cast<const uint4*>(gamma)[v], g);
+        if (beta != nullptr) vec_pairs<T>(reinterpret_cast<const uint4*>(beta)[v], c);
+#pragma unroll
+        for (int e = 0; e < PV; ++e) {
+            uint64_t o = f2_mul(f[i][e], rs2);
+            if (gamma != nullptr && beta != nullptr) o = f2_fma(o, g[e], c[e]);
+            else if (gamma != nullptr) o = f2_mul(o, g[e]);
+            else if (beta != nullptr) o = f2_add(o, c[e]);
+            f[i][e] = o;
+        }
+        y[v] = pairs_vec<T>(f[i]);
+    }
+}
+
+// The same for rows that are not whole vectors: element t, t + threads, ...
+template <typename T, int NV>
+__global__ void __launch_bounds__(1024) norm_fwd_scalar_kernel(const T* __restrict__ X,
+                                                              const T* __restrict__ gamma,
+                                                              const T* __restrict__ beta, T* __restrict__ Y,
+                                                              float* __restrict__ mean,
+                                                              float* __restrict__ rstd, int64_t R, int h,
+                                                              float inv_h, float eps) {
+    __shared__ float red[2][32];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+    if (r >= R) return;
+    const int nt = static_cast<int>(blockDim.x);
+    float f[NV], s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = threadIdx.x + i * nt;
+        f[i] = c < h ? to_f32<T>(X[r * h + c]) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) s += f[i];
+    const float mu = row_sum(s, red[0]) * inv_h;
+    float q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        f[i] -= mu;
+        if (static_cast<int>(threadIdx.x) + i * nt < h) q += f[i] * f[i];
+    }
+    const float rs = rsqrtf(row_sum(q, red[1]) * inv_h + eps);
+    if (threadIdx.x == 0 && mean != nullptr) {
+        mean[r] = mu;
+        rstd[r] = rs;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = threadIdx.x + i * nt;
+        if (c >= h) continue;
+        float o = f[i] * rs;
+        if (gamma != nullptr) o *= to_f32<T>(gamma[c]);
+        if (beta != nullptr) o += to_f32<T>(beta[c]);
+        Y[r * h + c] = from_f32<T>(o);
+    }
+}
+
+// Backward of rows that are not whole 16-byte vectors. Blocks walk the rows r =
+// block, block + grid, ...; a thread owns the same NV columns in every row and
+// keeps their dgamma and dbeta sums in registers, so the weight gradients cost
+// no second pass over the data: each block writes one row of partial sums,
+// which colsum_final2_kernel adds in block order.
+template <typename T, int NV>
+__global__ void __launch_bounds__(512) norm_bwd_kernel(const T* dY, const T* __restrict__ X,
+                                                       const T* __restrict__ gamma,
+                                                       const float* __restrict__ mean,
+                                                       const float* __restrict__ rstd, const T* dR, T* dX,
+                                                       float* __restrict__ part_g, float* __restrict__ part_b,
+                                                       int64_t R, int h) {
+    __shared__ float red[2][2][32];
+    grid_dep_wait();
+    grid_dep_launch();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nt = static_cast<int>(blockDim.x);
+    const float inv_h = 1.0f / static_cast<float>(h);
+    const bool in = lane < nt >> 5;
+    float ag[NV], ab[NV];
+    T rg[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = threadIdx.x + i * nt;
+        ag[i] = ab[i] = 0.0f;
+        rg[i] = gamma != nullptr && c < h ? gamma[c] : from_f32<T>(1.0f);
+    }
+    int turn = 0;
+    for (int64_t r = blockIdx.x; r < R; r += gridDim.x) {
+        const float mu = mean[r], rs = rstd[r];
+        const int64_t off = r * h;
+        T rx[NV], ry[NV], rd[NV];
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = threadIdx.x + i * nt;
+            rx[i] = ry[i] = rd[i] = from_f32<T>(0.0f);
+            if (c < h) {
+                rx[i] = X[off + c];
+                ry[i] = dY[off + c];
+                if (dR != nullptr) rd[i] = dR[off + c];
+            }
+        }
+        float c1 = 0.0f, c2 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            if (static_cast<int>(threadIdx.x) + i * nt >= h) continue;
+            const float y = to_f32<T>(ry[i]), xh = (to_f32<T>(rx[i]) - mu) * rs;
+            const float gy = y * to_f32<T>(rg[i]);
+            c1 += gy;
+            c2 += gy * xh;
+            ag[i] += y * xh;
+            ab[i] += y;
+        }
+        c1 = warp_sum(c1);
+        c2 = warp_sum(c2);
+        // two sets of slots in turn: one barrier per row
+        if (lane == 0) {
+            red[turn][0][warp] = c1;
+            red[turn][1][warp] = c2;
+        }
+        __syncthreads();
+        c1 = warp_sum(in ? red[turn][0][lane] : 0.0f) * inv_h;
+        c2 = warp_sum(in ? red[turn][1][lane] : 0.0f) * inv_h;
+        turn ^= 1;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = threadIdx.x + i * nt;
+            if (c >= h) continue;
+            const float xh = (to_f32<T>(rx[i]) - mu) * rs;
+            const float gy = to_f32<T>(ry[i]) * to_f32<T>(rg[i]);
+            dX[off + c] = from_f32<T>(rs * (gy - c1 - xh * c2) + to_f32<T>(rd[i]));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const int c = threadIdx.x + i * nt;
+        if (c < h) {
+            part_g[static_cast<int64_t>(blockIdx.x) * h + c] = ag[i];
+            part_b[static_cast<int64_t>(blockIdx.x) * h + c] = ab[i];
+        }
+    }
+}
+
 // Backward of rows that are whole 16-byte vectors. As norm_bwd_kernel, but the
 // rows arrive through a shared-memory ring of bulk copies, so the bytes in
 // flight do not depend on the registers a thread can spare: a row's X, dY and
-// dR are one stage, read for the sums and again for dX (kept in registers in
-// between they would spill: the two weight gradients' sums take two registers
-// per element). A group of threads (a warp, or the block) owns a ring and walks
+// dR are one stage, read for the sums and again for dX. A group of threads (a warp, or the block) owns a ring and walks
 // the rows group, group + groups, ...; a row's stage is refilled after the next
-// row's sums, whose barrier tells that every thread is through with it. Waits
-// are bounded.
+// row's sums, whose barrier tells that every thread is through with it (with one
+// stage, after a barrier of its own). KEEP: x̂ and dY ⊙ gamma stay in registers
+// between the two uses, up to 16 elements per thread. ONE: one stage, gamma read
+// from global memory (rows so wide that no more fits). Waits are bounded.
 struct NormRing {
-    int stages;  // rows a group's ring holds (2..8)
+    int stages;  // rows a group's ring holds (1..8)
     uint64_t wait_limit_ns;
 };
 
-template <typename T, int NV, bool WARP, int MAX_THREADS>
-__global__ void __launch_bounds__(MAX_THREADS) norm_bwd_ring_kernel(const T* dY, const T* __restrict__ X,
+template <typename T, int NV, bool WARP, int MAX_THREADS, int PER_SM, bool KEEP, bool ONE = false>
+__global__ void __launch_bounds__(MAX_THREADS, PER_SM) norm_bwd_ring_kernel(const T* dY, const T* __restrict__ X,
                                                             const T* __restrict__ gamma,
                                                             const float* __restrict__ mean,
                                                             const float* __restrict__ rstd, const T* dR, T* dX,
@@ -352,7 +297,7 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_bwd_ring_kernel(const T* dY,
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int groups = WARP ? static_cast<int>(blockDim.y) : 1;
     const int gi = WARP ? static_cast<int>(threadIdx.y) : 0;
-    const int S = ring.stages;
+    const int S = ONE ? 1 : ring.stages;
     uint64_t* full = bars + gi * 8;
     uint8_t* base = sm + static_cast<size_t>(gi) * S * stage_bytes;
     volatile int* abort = &abort_flag;
@@ -379,12 +324,11 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_bwd_ring_kernel(const T* dY,
         for (int s = 0; s < S && first + s * step < R; ++s) issue(first + s * step, s);
 
     const float inv_h = 1.0f / static_cast<float>(h);
-    // gamma behind the rings
+    const uint4* gg = reinterpret_cast<const uint4*>(gamma);
     uint4* sg = reinterpret_cast<uint4*>(sm + static_cast<size_t>(groups) * S * stage_bytes);
-    if (gamma != nullptr) {
+    if (!ONE && gamma != nullptr) {
         const int n = blockDim.x * blockDim.y;
-        for (int v = threadIdx.y * blockDim.x + threadIdx.x; v < nvec; v += n)
-            sg[v] = *reinterpret_cast<const uint4*>(gamma + v * VE);
+        for (int v = threadIdx.y * blockDim.x + threadIdx.x; v < nvec; v += n) sg[v] = gg[v];
         __syncthreads();
     }
     uint64_t ag[NV][PV], ab[NV][PV];
@@ -410,6 +354,7 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_bwd_ring_kernel(const T* dY,
         const bool got = mbar_wait_bounded(smem_u32(&full[at]), phase, abort, ring.wait_limit_ns);
         const uint64_t rs2 = f2_splat(rs), shift = f2_splat(-mu * rs);
         uint64_t s1 = 0ull, s2 = 0ull;
+        uint64_t kx[KEEP ? NV : 1][PV], ky[KEEP ? NV : 1][PV];
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int v = threadIdx.x + i * blockDim.x;
@@ -417,7 +362,7 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_bwd_ring_kernel(const T* dY,
             uint64_t x[PV], y[PV], g[PV];
             vec_pairs<T>(sx[v], x);
             vec_pairs<T>(sy[v], y);
-            if (gamma != nullptr) vec_pairs<T>(sg[v], g);
+            if (gamma != nullptr) vec_pairs<T>(ONE ? gg[v] : sg[v], g);
 #pragma unroll
             for (int e = 0; e < PV; ++e) {
                 const uint64_t xh = f2_fma(x[e], rs2, shift);
@@ -426,6 +371,10 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_bwd_ring_kernel(const T* dY,
                 s2 = f2_fma(gy, xh, s2);
                 ag[i][e] = f2_fma(y[e], xh, ag[i][e]);
                 ab[i][e] = f2_add(ab[i][e], y[e]);
+                if constexpr (KEEP) {
+                    kx[i][e] = xh;
+                    ky[i][e] = gy;
+                }
             }
         }
         float c1, c2, hi;
@@ -448,7 +397,7 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_bwd_ring_kernel(const T* dY,
         }
         if (failed) break;
         // every thread is through with the previous row's stage: S - 1 rows on
-        if (threadIdx.x == 0 && r > first && r + (S - 1) * step < R)
+        if (!ONE && threadIdx.x == 0 && r > first && r + (S - 1) * step < R)
             issue(r + (S - 1) * step, at == 0 ? S - 1 : at - 1);
         const uint64_t k1 = f2_splat(-rs * (c1 * inv_h)), k2 = f2_splat(-rs * (c2 * inv_h));
         T* out = dX + r * h;
@@ -457,19 +406,31 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_bwd_ring_kernel(const T* dY,
             const int v = threadIdx.x + i * blockDim.x;
             if (v >= nvec) continue;
             uint64_t x[PV], y[PV], g[PV], d[PV];
-            vec_pairs<T>(sx[v], x);
-            vec_pairs<T>(sy[v], y);
-            if (gamma != nullptr) vec_pairs<T>(sg[v], g);
+            if constexpr (!KEEP) {
+                vec_pairs<T>(sx[v], x);
+                vec_pairs<T>(sy[v], y);
+                if (gamma != nullptr) vec_pairs<T>(ONE ? gg[v] : sg[v], g);
+            }
             if (dR != nullptr) vec_pairs<T>(sr[v], d);
 #pragma unroll
             for (int e = 0; e < PV; ++e) {
-                const uint64_t xh = f2_fma(x[e], rs2, shift);
-                const uint64_t gy = gamma != nullptr ? f2_mul(y[e], g[e]) : y[e];
+                uint64_t xh, gy;
+                if constexpr (KEEP) {
+                    xh = kx[KEEP ? i : 0][e];
+                    gy = ky[KEEP ? i : 0][e];
+                } else {
+                    xh = f2_fma(x[e], rs2, shift);
+                    gy = gamma != nullptr ? f2_mul(y[e], g[e]) : y[e];
+                }
                 uint64_t o = f2_fma(xh, k2, f2_fma(gy, rs2, k1));
                 if (dR != nullptr) o = f2_add(o, d[e]);
                 x[e] = o;
             }
             *reinterpret_cast<uint4*>(out + v * VE) = pairs_vec<T>(x);
+        }
+        if constexpr (ONE) {
+            __syncthreads();
+            if (threadIdx.x == 0 && r + step < R) issue(r + step, 0);
         }
         if (++at == S) {
             at = 0;
@@ -481,7 +442,7 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_bwd_ring_kernel(const T* dY,
         if (threadIdx.x == 0) {
             // wind down: the copies still in flight, from this row's on (the
             // previous row's stage has not been filled again)
-            for (int q = 0; q < (r == first ? S : S - 1) && r + q * step < R; ++q) {
+            for (int q = 0; q < (r == first || ONE ? S : S - 1) && r + q * step < R; ++q) {
                 volatile int never = 0;
                 mbar_wait_bounded(smem_u32(&full[at]), phase, &never, ring.wait_limit_ns);
                 if (++at == S) {
@@ -559,7 +520,7 @@ __global__ void __launch_bounds__(1024) norm_fwd_wide_kernel(const T* __restrict
         const float d = to_f32<T>(x[c]) - mu;
         q += d * d;
     }
-    const float rs = 1.0f / sqrtf(row_sum(q, red[1]) / static_cast<float>(h) + eps);
+    const float rs = rsqrtf(row_sum(q, red[1]) / static_cast<float>(h) + eps);
     if (threadIdx.x == 0 && mean != nullptr) {
         mean[r] = mu;
         rstd[r] = rs;
