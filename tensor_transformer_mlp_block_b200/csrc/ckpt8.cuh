@@ -47,16 +47,18 @@ __device__ __forceinline__ float c8_scale(uint32_t s) {
     return __uint_as_float(s == 0u ? 0x00400000u : s << 23);
 }
 
-// Four values to four int8: x·inv + 1.5·2^23 is rounded once, to an integer
-// (ties to even), whose low byte is the two's complement wanted. A block
-// marked NaN stores zeros.
+// Rounding: x·inv + 1.5·2^23 is rounded once, to an integer (ties to even), whose
+// low byte is the two's complement wanted. (A block marked NaN stores zeros.)
+constexpr float kC8Round = 12582912.0f;
+
+__device__ __forceinline__ uint32_t c8_gather4(float t0, float t1, float t2, float t3) {
+    return __byte_perm(__byte_perm(__float_as_uint(t0), __float_as_uint(t1), 0x0040),
+                       __byte_perm(__float_as_uint(t2), __float_as_uint(t3), 0x0040), 0x5410);
+}
+
 __device__ __forceinline__ uint32_t c8_pack4(float x0, float x1, float x2, float x3, float inv) {
-    constexpr float kRound = 12582912.0f;
-    const uint32_t t0 = __float_as_uint(__fmaf_rn(x0, inv, kRound));
-    const uint32_t t1 = __float_as_uint(__fmaf_rn(x1, inv, kRound));
-    const uint32_t t2 = __float_as_uint(__fmaf_rn(x2, inv, kRound));
-    const uint32_t t3 = __float_as_uint(__fmaf_rn(x3, inv, kRound));
-    return __byte_perm(__byte_perm(t0, t1, 0x0040), __byte_perm(t2, t3, 0x0040), 0x5410);
+    return c8_gather4(__fmaf_rn(x0, inv, kC8Round), __fmaf_rn(x1, inv, kC8Round), __fmaf_rn(x2, inv, kC8Round),
+                      __fmaf_rn(x3, inv, kC8Round));
 }
 
 // The integers of four int8 as floats (exact): byte + 128 in the low mantissa

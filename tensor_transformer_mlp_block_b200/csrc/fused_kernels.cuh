@@ -78,8 +78,33 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const T* __restrict__ dY,
     const int64_t r0 = static_cast<int64_t>(blockIdx.x) * rows_per_chunk;
     const int64_t r1 = min(R, r0 + rows_per_chunk);
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 2
-    for (int64_t r = r0 + threadIdx.y; r < r1; r += 8) {
+    // the loads of kU rows are issued before any of them is used
+    constexpr int kU = sizeof(T) == 2 && VEC ? 4 : 1;
+    int64_t r = r0 + threadIdx.y;
+    if constexpr (kU > 1) {
+        for (; c0 < C && r + 8 * (kU - 1) < r1; r += 8 * kU) {
+            uint4 ry[kU], rx[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                ry[u] = *reinterpret_cast<const uint4*>(dY + (r + 8 * u) * C + c0);
+                rx[u] = *reinterpret_cast<const uint4*>(H + (r + 8 * u) * C + c0);
+            }
+#pragma unroll
+            for (int u = 0; u < kU; ++u) {
+                float y[8], x[8], d[8];
+                unpack_bf16x8(ry[u], y);
+                unpack_bf16x8(rx[u], x);
+                act_grad8<T, TANH>(x, d);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    y[i] *= d[i];
+                    acc[i] += y[i];
+                }
+                store8<T, VEC>(dH + (r + 8 * u) * C, c0, C, y);
+            }
+        }
+    }
+    for (; r < r1; r += 8) {
         float y[8], x[8], d[8];
         load8<T, VEC>(dY + r * C, c0, C, y);
         load8<T, VEC>(H + r * C, c0, C, x);
@@ -109,13 +134,10 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const T* __restrict__ dY,
 // tile's 256 scale bytes are gathered in shared memory and written 32 to a row
 // of S (one row of the tile each would touch a 32-byte sector per byte).
 
-// H of type TI (bias, if given, is added to it: the plain path's product) to
-// C and S; ACT: 0 none, 1 GeLU, 2 its tanh form, written to Y.
-template <typename TI, typename T, int ACT, bool VEC>
-__global__ void __launch_bounds__(256) ckpt8_encode_kernel(const TI* __restrict__ H,
-                                                           const T* __restrict__ bias, T* __restrict__ Y,
-                                                           uint8_t* __restrict__ C, uint8_t* __restrict__ S,
-                                                           int64_t R, int64_t F) {
+// H to C and S.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) ckpt8_encode_kernel(const T* __restrict__ H, uint8_t* __restrict__ C,
+                                                           uint8_t* __restrict__ S, int64_t R, int64_t F) {
     __shared__ uint8_t sS[8][32];
     grid_dep_wait();
     grid_dep_launch();
@@ -123,18 +145,12 @@ __global__ void __launch_bounds__(256) ckpt8_encode_kernel(const TI* __restrict_
     const int64_t ldc = (F + kC8Block - 1) / kC8Block * kC8Block;
     const int64_t row0 = static_cast<int64_t>(blockIdx.x) * 32;
     const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + lane * 8;
-    float bb[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (bias != nullptr) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i < F) bb[i] = to_f32<T>(bias[c + i]);
-    }
     float h[4][8];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int64_t r = row0 + warp + 8 * k;
         if (r < R) {
-            load8<TI, VEC>(H + r * F, c, F, h[k]);
+            load8<T, VEC>(H + r * F, c, F, h[k]);
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) h[k][i] = 0.0f;
@@ -145,10 +161,7 @@ __global__ void __launch_bounds__(256) ckpt8_encode_kernel(const TI* __restrict_
         const int64_t r = row0 + warp + 8 * k;
         float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            h[k][i] += bb[i];
-            top = max_nan(top, fabsf(h[k][i]));
-        }
+        for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(h[k][i]));
         top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const uint32_t sb = c8_scale_byte(top);
@@ -158,36 +171,29 @@ __global__ void __launch_bounds__(256) ckpt8_encode_kernel(const TI* __restrict_
         if (sb == kC8NaN) w = make_uint2(0u, 0u);
         if ((lane & 3) == 0) sS[lane >> 2][warp + 8 * k] = static_cast<uint8_t>(sb);
         if (r < R && c < ldc) *reinterpret_cast<uint2*>(C + r * ldc + c) = w;
-        if constexpr (ACT != 0) {
-            float y[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) y[i] = ACT == 2 ? gelu_tanh_f32(h[k][i]) : gelu_f32(h[k][i]);
-            if (r < R) store8<T, VEC>(Y + r * F, c, F, y);
-        }
     }
     __syncthreads();
     const int64_t block = static_cast<int64_t>(blockIdx.y) * 8 + warp;
     if (block * kC8Block < F && row0 + lane < R) S[block * R + row0 + lane] = sS[warp][lane];
 }
 
-// The values C and S stand for (P null: written to out0 as T), or, for the
-// plain path's backward, dH = P ⊙ act′(H̃) to out0 and Y = act(H̃) to out1.
-template <typename T, int ACT, bool VEC>
+// The values C and S stand for.
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) ckpt8_decode_kernel(const uint8_t* __restrict__ C,
-                                                           const uint8_t* __restrict__ S,
-                                                           const float* __restrict__ P, T* __restrict__ out0,
-                                                           T* __restrict__ out1, int64_t R, int64_t F) {
+                                                           const uint8_t* __restrict__ S, T* __restrict__ H,
+                                                           int64_t R, int64_t F) {
     grid_dep_wait();
     grid_dep_launch();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t ldc = (F + kC8Block - 1) / kC8Block * kC8Block;
+    const int64_t row0 = static_cast<int64_t>(blockIdx.x) * 32;
     const int64_t c = static_cast<int64_t>(blockIdx.y) * 256 + lane * 8;
     if (c >= F) return;
     uint2 w[4];
     uint32_t sb[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const int64_t r = static_cast<int64_t>(blockIdx.x) * 32 + warp + 8 * k;
+        const int64_t r = row0 + warp + 8 * k;
         w[k] = make_uint2(0u, 0u);
         sb[k] = 0u;
         if (r < R) {
@@ -197,25 +203,13 @@ __global__ void __launch_bounds__(256) ckpt8_decode_kernel(const uint8_t* __rest
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-        const int64_t r = static_cast<int64_t>(blockIdx.x) * 32 + warp + 8 * k;
+        const int64_t r = row0 + warp + 8 * k;
         if (r >= R) continue;
         const float s = c8_scale(sb[k]);
         float x[8];
         c8_unpack4(w[k].x, s, x);
         c8_unpack4(w[k].y, s, x + 4);
-        if constexpr (ACT == 0) {
-            store8<T, VEC>(out0 + r * F, c, F, x);
-        } else {
-            float p[8], y[8];
-            load8<float, VEC>(P + r * F, c, F, p);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                p[i] *= ACT == 2 ? gelu_tanh_grad_f32(x[i]) : gelu_grad_f32(x[i]);
-                y[i] = ACT == 2 ? gelu_tanh_f32(x[i]) : gelu_f32(x[i]);
-            }
-            store8<T, VEC>(out0 + r * F, c, F, p);
-            store8<T, VEC>(out1 + r * F, c, F, y);
-        }
+        store8<T, VEC>(H + r * F, c, F, x);
     }
 }
 
@@ -223,17 +217,67 @@ __global__ void __launch_bounds__(256) ckpt8_decode_kernel(const uint8_t* __rest
 // The CUDA-core product of simt.cuh with register tiles: BT × BT outputs per
 // block of 256 threads, TM × TM each (TM = BT/16), 16-deep k tiles in shared
 // memory, the next tile's global loads in flight during the current one's
-// arithmetic. Each output is one fp32 accumulator updated with fmaf over k in
-// ascending order, so the result is bitwise that of simt_gemm_kernel.
-// TI: operands, bias and residual; TO: outputs.
+// arithmetic. Each output is an fp32 accumulator updated with fmaf over k in
+// ascending order; with S > 1 (BT = 64) a cluster of S blocks takes consecutive
+// parts of K, and each block adds the parts of its 64/S rows in ascending k
+// (few output tiles and a long K: weight gradients of narrow layers, single
+// tokens). A launch may hold a second product of the same kind, whose tiles
+// follow the first's.
+struct TiledProduct {
+    SimtArgs a;
+    const void* resid;  // kResid: M × N of the operands' type, row stride ld_out; may be null
+    uint8_t* c8;        // kC8Out, kC8In: the 8-bit checkpoint (ckpt8.cuh)
+    uint8_t* c8_scale;
+    int64_t c8_ld;
+    int mb, nb;         // tiles
+};
+
+// Output (m, n) of a product from its sum.
+template <typename TI, typename TO, int EPI>
+__device__ __forceinline__ void tiled_store(const TiledProduct& p, int64_t m, int64_t n, float v) {
+    const SimtArgs& g = p.a;
+    const int64_t off = m * g.ld_out + n;
+    if constexpr (EpiTraits<EPI>::kBias && !EpiTraits<EPI>::kC8Out) {
+        if (g.bias != nullptr) v += ld_f32<TI>(static_cast<const TI*>(g.bias) + n);
+    }
+    float res = 0.0f;
+    if constexpr (EpiTraits<EPI>::kResid) {
+        if (p.resid != nullptr) res = ld_f32<TI>(static_cast<const TI*>(p.resid) + off);
+    }
+    if constexpr (EpiTraits<EPI>::kC8In) {
+        const float h = static_cast<float>(static_cast<int8_t>(p.c8[m * p.c8_ld + n])) *
+                        c8_scale(p.c8_scale[n / kC8Block * g.M + m]);
+        static_cast<TO*>(g.out0)[off] =
+            from_f32<TO>(v * (EpiTraits<EPI>::kTanh ? gelu_tanh_grad_f32(h) : gelu_grad_f32(h)));
+        static_cast<TO*>(g.out1)[off] = from_f32<TO>(EpiTraits<EPI>::kTanh ? gelu_tanh_f32(h) : gelu_f32(h));
+    } else if constexpr (EpiTraits<EPI>::kAct) {
+        static_cast<TO*>(g.out0)[off] = from_f32<TO>(v);
+        static_cast<TO*>(g.out1)[off] =
+            from_f32<TO>((EpiTraits<EPI>::kTanh ? gelu_tanh_f32(v) : gelu_f32(v)) + res);
+    } else {
+        if constexpr (EpiTraits<EPI>::kActOnly) v = EpiTraits<EPI>::kTanh ? gelu_tanh_f32(v) : gelu_f32(v);
+        static_cast<TO*>(g.out0)[off] = from_f32<TO>(v + res);
+    }
+}
+
 template <typename TI, typename TO, int EPI, int BT>
-__global__ void __launch_bounds__(256) simt_tiled_kernel(const SimtArgs g, const TI* resid) {
+__global__ void __launch_bounds__(256) simt_tiled_kernel(const TiledProduct p0, const TiledProduct p1, int S) {
     constexpr int TM = BT / 16, BK = 16, LD = BT + 4;
     __shared__ float sA[2][BK][LD];
     __shared__ float sB[2][BK][LD];
+    __shared__ float parts[BT == 64 ? 64 * 64 : 1];  // [rank][row of this block's][column]
+    const int tiles0 = p0.mb * p0.nb;
+    const bool second = static_cast<int>(blockIdx.x) >= tiles0;
+    const TiledProduct& p = second ? p1 : p0;
+    const SimtArgs& g = p.a;
+    const int tile = static_cast<int>(blockIdx.x) - (second ? tiles0 : 0);
     const int t = threadIdx.x;
     const int tx = t & 15, ty = t >> 4;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * BT, n0 = static_cast<int64_t>(blockIdx.y) * BT;
+    const int64_t m0 = static_cast<int64_t>(tile % p.mb) * BT, n0 = static_cast<int64_t>(tile / p.mb) * BT;
+    const int rank = static_cast<int>(blockIdx.z);
+    const int steps = (g.K + BK - 1) / BK;
+    const int kbeg = static_cast<int>(static_cast<int64_t>(rank) * steps / S) * BK;
+    const int kend = min(g.K, static_cast<int>(static_cast<int64_t>(rank + 1) * steps / S) * BK);
     const TI* A = static_cast<const TI*>(g.A);
     const TI* B = static_cast<const TI*>(g.B);
     // consecutive threads along the operand's unit stride
@@ -245,8 +289,8 @@ __global__ void __launch_bounds__(256) simt_tiled_kernel(const SimtArgs g, const
             const int e = t + 256 * i;
             const int am = a_k ? e / BK : e % BT, ak = a_k ? e % BK : e / BT;
             const int bn = b_k ? e / BK : e % BT, bk = b_k ? e % BK : e / BT;
-            ra[i] = (m0 + am < g.M && k0 + ak < g.K) ? ld_f32<TI>(A + (m0 + am) * g.sam + (k0 + ak) * g.sak) : 0.0f;
-            rb[i] = (n0 + bn < g.N && k0 + bk < g.K) ? ld_f32<TI>(B + (k0 + bk) * g.sbk + (n0 + bn) * g.sbn) : 0.0f;
+            ra[i] = (m0 + am < g.M && k0 + ak < kend) ? ld_f32<TI>(A + (m0 + am) * g.sam + (k0 + ak) * g.sak) : 0.0f;
+            rb[i] = (n0 + bn < g.N && k0 + bk < kend) ? ld_f32<TI>(B + (k0 + bk) * g.sbk + (n0 + bn) * g.sbn) : 0.0f;
         }
     };
     auto stash = [&](int buf) {
@@ -264,14 +308,13 @@ __global__ void __launch_bounds__(256) simt_tiled_kernel(const SimtArgs g, const
     for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TM; ++j) acc[i][j] = 0.0f;
-    fetch(0);
+    fetch(kbeg);
     stash(0);
     __syncthreads();
     int buf = 0;
-    for (int k0 = 0; k0 < g.K; k0 += BK) {
-        if (k0 + BK < g.K) fetch(k0 + BK);
-        // terms beyond K are zero products of an exact zero accumulator step:
-        // fmaf(0, 0, acc) leaves acc as it is
+    for (int k0 = kbeg; k0 < kend; k0 += BK) {
+        if (k0 + BK < kend) fetch(k0 + BK);
+        // terms beyond the range are fmaf(0, 0, acc), which leaves acc as it is
 #pragma unroll
         for (int k = 0; k < BK; ++k) {
             float a[TM], b[TM];
@@ -285,41 +328,62 @@ __global__ void __launch_bounds__(256) simt_tiled_kernel(const SimtArgs g, const
 #pragma unroll
                 for (int j = 0; j < TM; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
         }
-        if (k0 + BK < g.K) {
+        if (k0 + BK < kend) {
             stash(buf ^ 1);
             __syncthreads();
             buf ^= 1;
         }
     }
+    if constexpr (BT == 64) {
+        if (S > 1) {
+            const int own = 64 / S;  // rows per block; S divides 64
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 4 * ty + i;
+                const uint32_t dst = mapa_shared(smem_u32(parts + (rank * own + row % own) * 64 + 4 * tx), row / own);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) st_shared_cluster_u32(dst + 4 * j, __float_as_uint(acc[i][j]));
+            }
+            cluster_sync();  // every block's sums of this block's rows have arrived
+            for (int e = t; e < own * 64; e += 256) {
+                const int row = e / 64, col = e % 64;
+                float v = parts[row * 64 + col];
+                for (int q = 1; q < S; ++q) v += parts[(q * own + row) * 64 + col];
+                const int64_t m = m0 + rank * own + row, n = n0 + col;
+                if (m < g.M && n < g.N) tiled_store<TI, TO, EPI>(p, m, n, v);
+            }
+            return;
+        }
+    }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
         const int64_t m = m0 + 16 * (i & ~3) + 4 * ty + (i & 3);
+        if constexpr (EpiTraits<EPI>::kC8Out) {
+            // 32 columns of a row are 8 neighbouring threads' groups of four
+#pragma unroll
+            for (int j = 0; j < TM; j += 4) {
+                const int64_t n = n0 + 16 * j + 4 * tx;
+                float top = 0.0f;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    if (g.bias != nullptr && n + c < g.N)
+                        acc[i][j + c] += ld_f32<TI>(static_cast<const TI*>(g.bias) + n + c);
+                    top = max_nan(top, fabsf(acc[i][j + c]));
+                }
+                for (int w = 1; w < 8; w <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, w));
+                const uint32_t sb = c8_scale_byte(top);
+                const uint32_t word = sb == kC8NaN ? 0u : c8_pack4(acc[i][j], acc[i][j + 1], acc[i][j + 2],
+                                                                   acc[i][j + 3], c8_inverse(sb));
+                if (m < g.M && n < p.c8_ld) *reinterpret_cast<uint32_t*>(p.c8 + m * p.c8_ld + n) = word;
+                if (m < g.M && n < g.N && (tx & 7) == 0)
+                    p.c8_scale[n / kC8Block * g.M + m] = static_cast<uint8_t>(sb);
+            }
+        }
         if (m >= g.M) continue;
 #pragma unroll
         for (int j = 0; j < TM; ++j) {
             const int64_t n = n0 + 16 * (j & ~3) + 4 * tx + (j & 3);
-            if (n >= g.N) continue;
-            const int64_t off = m * g.ld_out + n;
-            float v = acc[i][j];
-            if constexpr (EpiTraits<EPI>::kBias) {
-                if (g.bias != nullptr) v += ld_f32<TI>(static_cast<const TI*>(g.bias) + n);
-            }
-            if constexpr (EpiTraits<EPI>::kDAct) {
-                const float hv = ld_f32<TI>(static_cast<const TI*>(g.aux) + off);
-                v *= EpiTraits<EPI>::kTanh ? gelu_tanh_grad_f32(hv) : gelu_grad_f32(hv);
-            }
-            float res = 0.0f;
-            if constexpr (EpiTraits<EPI>::kResid) {
-                if (resid != nullptr) res = ld_f32<TI>(resid + off);
-            }
-            if constexpr (EpiTraits<EPI>::kAct) {
-                static_cast<TO*>(g.out0)[off] = from_f32<TO>(v);
-                const float y = EpiTraits<EPI>::kTanh ? gelu_tanh_f32(v) : gelu_f32(v);
-                static_cast<TO*>(g.out1)[off] = from_f32<TO>(y + res);
-            } else {
-                if constexpr (EpiTraits<EPI>::kActOnly) v = EpiTraits<EPI>::kTanh ? gelu_tanh_f32(v) : gelu_f32(v);
-                static_cast<TO*>(g.out0)[off] = from_f32<TO>(v + res);
-            }
+            if (n < g.N) tiled_store<TI, TO, EPI>(p, m, n, acc[i][j]);
         }
     }
 }

@@ -23,34 +23,64 @@ bool fits32(int64_t x) { return x < (int64_t(1) << 31); }
 
 // ------------------------------------------------------------- plain products
 
-// Tiles of simt_tiled_kernel: 128 × 128 (8 × 8 outputs a thread) where that
-// still leaves two tiles per SM, else 64 × 64.
+// One product, or two of the same kind in one launch (q may be null). Tiles
+// of 128 × 128 (8 × 8 outputs a thread) where they still are two per SM, else
+// 64 × 64; with fewer of those than SMs, K is split over a cluster of up to 8
+// blocks (at least four 16-deep steps each).
 template <typename TI, typename TO, int EPI>
-tpmlp_status gemm_plain(int kind, const SimtArgs& a, const TI* resid, cudaStream_t st) {
-    const double flops = 2.0 * a.M * a.N * a.K;
-    const double bytes = sizeof(TI) * (1.0 * a.M * a.K + 1.0 * a.K * a.N) + 1.0 * sizeof(TO) * a.M * a.N;
-    const int64_t tiles128 = ((int64_t(a.M) + 127) / 128) * ((int64_t(a.N) + 127) / 128);
-    const int bt = tiles128 >= 2 * plan_num_sms() ? 128 : 64;
-    const int64_t gx = (int64_t(a.M) + bt - 1) / bt, gy = (int64_t(a.N) + bt - 1) / bt;
-    if (gy > kMaxGridY) return TPMLP_ERR_UNSUPPORTED;
+tpmlp_status gemm_plain(int kind, TiledProduct p, cudaStream_t st, const TiledProduct* q = nullptr) {
+    double flops = 0.0, bytes = 0.0;
+    int64_t tiles128 = 0, tiles64 = 0, k = p.a.K;
+    for (const TiledProduct* x : {static_cast<const TiledProduct*>(&p), q}) {
+        if (x == nullptr) continue;
+        const double M = x->a.M, N = x->a.N, K = x->a.K;
+        flops += 2.0 * M * N * K;
+        bytes += sizeof(TI) * (M * K + K * N) + sizeof(TO) * M * N;
+        tiles128 += ((int64_t(x->a.M) + 127) / 128) * ((int64_t(x->a.N) + 127) / 128);
+        tiles64 += ((int64_t(x->a.M) + 63) / 64) * ((int64_t(x->a.N) + 63) / 64);
+    }
+    const int sms = plan_num_sms();
+    const int bt = tiles128 >= 2 * sms ? 128 : 64;
+    int S = 1;
+    if (bt == 64 && !EpiTraits<EPI>::kC8Out)
+        while (S < 8 && tiles64 * S * 2 <= 2 * sms && k >= 128 * S) S *= 2;
+    TiledProduct none{};
+    TiledProduct p1 = q != nullptr ? *q : none;
+    for (TiledProduct* x : {&p, &p1}) {
+        x->mb = (x->a.M + bt - 1) / bt;
+        x->nb = (x->a.N + bt - 1) / bt;
+    }
     return timed(kind, flops, bytes, st, [&] {
-        const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
-        if (bt == 128)
-            simt_tiled_kernel<TI, TO, EPI, 128><<<grid, 256, 0, st>>>(a, resid);
-        else
-            simt_tiled_kernel<TI, TO, EPI, 64><<<grid, 256, 0, st>>>(a, resid);
-        return check_launch();
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(bt == 128 ? tiles128 : tiles64), 1, static_cast<unsigned>(S));
+        cfg.blockDim = dim3(256);
+        cfg.stream = st;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = 1;
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = static_cast<unsigned>(S);
+        cfg.attrs = &attr;
+        cfg.numAttrs = S > 1 ? 1 : 0;
+        const cudaError_t e = bt == 128 ? cudaLaunchKernelEx(&cfg, simt_tiled_kernel<TI, TO, EPI, 128>, p, p1, S)
+                                        : cudaLaunchKernelEx(&cfg, simt_tiled_kernel<TI, TO, EPI, 64>, p, p1, S);
+        g_launches.fetch_add(1, std::memory_order_relaxed);
+        if (e != cudaSuccess) cudaGetLastError();
+        return e == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
     });
 }
 
-// Column-tile limits of the plain products and the element-wise kernels (grid
-// y), checked before a call's first launch.
-bool plain_grid_ok(int64_t n) { return (n + 63) / 64 <= kMaxGridY; }
+// Tiles of a plain product fit the grid (checked before a call's first launch).
+bool plain_grid_ok(int64_t M, int64_t N) { return ((M + 63) / 64) * ((N + 63) / 64) < (int64_t(1) << 31); }
+
+// Column tiles of the element-wise kernels (grid y) fit the grid.
+bool columns_ok(int64_t n) { return (n + 255) / 256 <= kMaxGridY; }
 
 // Aop(m, k), Bop(k, n) of one product by strides.
-SimtArgs plain_args(int64_t M, int64_t N, int64_t K, const void* A, int64_t sam, int64_t sak, const void* B,
-                    int64_t sbk, int64_t sbn, void* out) {
-    SimtArgs a{};
+TiledProduct plain_args(int64_t M, int64_t N, int64_t K, const void* A, int64_t sam, int64_t sak, const void* B,
+                        int64_t sbk, int64_t sbn, void* out) {
+    TiledProduct p{};
+    SimtArgs& a = p.a;
     a.M = static_cast<int>(M);
     a.N = static_cast<int>(N);
     a.K = static_cast<int>(K);
@@ -62,7 +92,7 @@ SimtArgs plain_args(int64_t M, int64_t N, int64_t K, const void* A, int64_t sam,
     a.sbn = sbn;
     a.out0 = out;
     a.ld_out = N;
-    return a;
+    return p;
 }
 
 // ------------------------------------------------------------------ layer norm
@@ -374,19 +404,13 @@ tpmlp_status linear_ex_tc(const void* X, const void* W, int T, int N, int K, con
     return gemm_tc<256, false, true, EPI>(K_L_FWD, X, W, T, N, K, req, g, st);
 }
 
-template <typename T, int EPI>
-tpmlp_status linear_ex_plain(const SimtArgs& a, const void* R, cudaStream_t st) {
-    return gemm_plain<T, T, EPI>(K_L_FWD, a, static_cast<const T*>(R), st);
-}
-
 template <typename T>
-tpmlp_status linear_ex_plain_any(tpmlp_activation act, bool keep, const SimtArgs& a, const void* R,
-                                 cudaStream_t st) {
-    if (act == TPMLP_ACT_NONE) return linear_ex_plain<T, EPI_ADD>(a, R, st);
+tpmlp_status linear_ex_plain(tpmlp_activation act, bool keep, const TiledProduct& p, cudaStream_t st) {
+    if (act == TPMLP_ACT_NONE) return gemm_plain<T, T, EPI_ADD>(K_L_FWD, p, st);
     if (act == TPMLP_GELU_ERF)
-        return keep ? linear_ex_plain<T, EPI_GELU_ADD>(a, R, st) : linear_ex_plain<T, EPI_ACT_ADD>(a, R, st);
-    return keep ? linear_ex_plain<T, EPI_GELU_ADD_TANH>(a, R, st)
-                : linear_ex_plain<T, EPI_ACT_ADD_TANH>(a, R, st);
+        return keep ? gemm_plain<T, T, EPI_GELU_ADD>(K_L_FWD, p, st) : gemm_plain<T, T, EPI_ACT_ADD>(K_L_FWD, p, st);
+    return keep ? gemm_plain<T, T, EPI_GELU_ADD_TANH>(K_L_FWD, p, st)
+                : gemm_plain<T, T, EPI_ACT_ADD_TANH>(K_L_FWD, p, st);
 }
 
 tpmlp_status linear_fwd_ex_impl(const void* X, const void* W, const void* bias, const void* R, void* H, void* Y,
@@ -426,12 +450,13 @@ tpmlp_status linear_fwd_ex_impl(const void* X, const void* W, const void* bias, 
         return R ? linear_ex_tc<EPI_GELU_ADD_TANH>(X, W, iT, iN, iK, req, g, st)
                  : linear_ex_tc<EPI_GELU_TANH>(X, W, iT, iN, iK, req, g, st);
     }
-    if (!plain_grid_ok(N)) return TPMLP_ERR_UNSUPPORTED;
-    SimtArgs a = plain_args(T, N, K, X, K, 1, W, N, 1, H != nullptr ? H : Y);
-    a.out1 = Y;
-    a.bias = bias;
-    if (dt == TPMLP_FP32) return linear_ex_plain_any<float>(act, H != nullptr, a, R, st);
-    return linear_ex_plain_any<bf16>(act, H != nullptr, a, R, st);
+    if (!plain_grid_ok(T, N)) return TPMLP_ERR_UNSUPPORTED;
+    TiledProduct q = plain_args(T, N, K, X, K, 1, W, N, 1, H != nullptr ? H : Y);
+    q.a.out1 = Y;
+    q.a.bias = bias;
+    q.resid = R;
+    if (dt == TPMLP_FP32) return linear_ex_plain<float>(act, H != nullptr, q, st);
+    return linear_ex_plain<bf16>(act, H != nullptr, q, st);
 }
 
 template <typename T, bool TANH>
@@ -485,53 +510,37 @@ tpmlp_status linear_bwd_ex_run(const LinPlan& pl, const void* dY, const void* X,
             return gemm_tc<256, false, false, EPI_BIAS>(K_L_DX, g, W, iT, iK, iN, pl.dx, gx, st);
         }
     }
-    TPMLP_TRY((gemm_plain<T, TG, EPI_F32>(K_L_DW, plain_args(K, N, R, X, 1, K, g, N, 1, dW), nullptr, st)));
-    return gemm_plain<T, T, EPI_F32>(K_L_DX, plain_args(R, K, N, g, N, 1, W, 1, N, dX), nullptr, st);
+    TPMLP_TRY((gemm_plain<T, TG, EPI_F32>(K_L_DW, plain_args(K, N, R, X, 1, K, g, N, 1, dW), st)));
+    return gemm_plain<T, T, EPI_F32>(K_L_DX, plain_args(R, K, N, g, N, 1, W, 1, N, dX), st);
 }
 
 // ------------------------------------------------------------ 8-bit checkpoint
 
 int64_t c8_blocks(int64_t F) { return (F + kC8Block - 1) / kC8Block; }
 
-template <typename TI, typename T, int ACT>
-tpmlp_status ckpt8_encode_launch(const void* H, const void* bias, void* Y, void* C, void* S, int64_t R, int64_t F,
-                                 cudaStream_t st) {
+template <typename T>
+tpmlp_status ckpt8_encode_launch(const void* H, void* C, void* S, int64_t R, int64_t F, cudaStream_t st) {
     const dim3 grid(static_cast<unsigned>((R + 31) / 32), static_cast<unsigned>((F + 255) / 256));
-    const bool vec = F % 8 == 0 && aligned16(H) && aligned16(Y);
-    auto kern = vec ? ckpt8_encode_kernel<TI, T, ACT, true> : ckpt8_encode_kernel<TI, T, ACT, false>;
-    return launch_dep(kern, grid, dim3(256), 0, st, static_cast<const TI*>(H), static_cast<const T*>(bias),
-                      static_cast<T*>(Y), static_cast<uint8_t*>(C), static_cast<uint8_t*>(S), R, F);
+    auto kern = F % 8 == 0 && aligned16(H) ? ckpt8_encode_kernel<T, true> : ckpt8_encode_kernel<T, false>;
+    return launch_dep(kern, grid, dim3(256), 0, st, static_cast<const T*>(H), static_cast<uint8_t*>(C),
+                      static_cast<uint8_t*>(S), R, F);
 }
 
-template <typename T, int ACT>
-tpmlp_status ckpt8_decode_launch(const void* C, const void* S, const float* P, void* out0, void* out1, int64_t R,
-                                 int64_t F, cudaStream_t st) {
+template <typename T>
+tpmlp_status ckpt8_decode_launch(const void* C, const void* S, void* H, int64_t R, int64_t F, cudaStream_t st) {
     const dim3 grid(static_cast<unsigned>((R + 31) / 32), static_cast<unsigned>((F + 255) / 256));
-    const bool vec = F % 8 == 0 && aligned16(P) && aligned16(out0) && aligned16(out1);
-    auto kern = vec ? ckpt8_decode_kernel<T, ACT, true> : ckpt8_decode_kernel<T, ACT, false>;
-    return launch_dep(kern, grid, dim3(256), 0, st, static_cast<const uint8_t*>(C), static_cast<const uint8_t*>(S),
-                      P, static_cast<T*>(out0), static_cast<T*>(out1), R, F);
-}
-
-// The MLP's plan plus, on the plain path, one T × F fp32 product (before the
-// activation is applied and H quantised, or dZ·Bᵀ).
-bool make_c8_plan(int64_t T, int64_t h, int64_t F, int p, tpmlp_dtype dt, Plan* pl, size_t* off_prod,
-                  size_t* total) {
-    if (!make_plan(T, h, F, p, dt, pl)) return false;
-    *off_prod = pl->total;
-    *total = pl->total + (pl->tc ? 0 : round256(static_cast<size_t>(T) * F * sizeof(float)));
-    return true;
+    auto kern = F % 8 == 0 && aligned16(H) ? ckpt8_decode_kernel<T, true> : ckpt8_decode_kernel<T, false>;
+    return launch_dep(kern, grid, dim3(256), 0, st, static_cast<const uint8_t*>(C),
+                      static_cast<const uint8_t*>(S), static_cast<T*>(H), R, F);
 }
 
 tpmlp_status c8_checks(int64_t T, int64_t h, int64_t F, int p, tpmlp_dtype dt, tpmlp_activation act, Plan* pl,
-                       size_t* off_prod, void* ws, size_t ws_bytes) {
-    size_t total = 0;
-    if (!make_c8_plan(T, h, F, p, dt, pl, off_prod, &total) || !known_act(act)) return TPMLP_ERR_INVALID;
-    if (!fits32(T) || !fits32(h) || !fits32(F) || !plain_grid_ok(F) || !plain_grid_ok(h))
+                       void* ws, size_t ws_bytes) {
+    if (!known_act(act)) return TPMLP_ERR_INVALID;
+    TPMLP_TRY(common_checks(T, h, F, p, dt, pl, ws, ws_bytes));
+    if (!plain_grid_ok(T, F) || !plain_grid_ok(T, h) || !plain_grid_ok(h, F) || pl->chunks > kMaxGridY)
         return TPMLP_ERR_UNSUPPORTED;
-    TPMLP_TRY(check_device());
-    if (total > 0 && (ws == nullptr || ws_bytes < total)) return TPMLP_ERR_WORKSPACE;
-    return ws != nullptr && !aligned16(ws) ? TPMLP_ERR_ALIGN : TPMLP_OK;
+    return TPMLP_OK;
 }
 
 template <int EPI>
@@ -564,18 +573,25 @@ tpmlp_status c8_fwd_tc(const Plan& pl, const void* X, const void* A, const void*
     return gemm_tc<256, false, true, EPI_BIAS>(K_F2, Y, B, iT, ih, iF, pl.f2, g2, st);
 }
 
+void set_c8(TiledProduct& p, const void* C, const void* S, int64_t F) {
+    p.c8 = static_cast<uint8_t*>(const_cast<void*>(C));
+    p.c8_scale = static_cast<uint8_t*>(const_cast<void*>(S));
+    p.c8_ld = c8_blocks(F) * kC8Block;
+}
+
 template <typename T>
 tpmlp_status c8_fwd_plain(const void* X, const void* A, const void* a, const void* B, const void* b, const void* R,
-                          void* C, void* S, void* Y, void* Z, float* prod, int64_t rows, int64_t h, int64_t F,
+                          void* C, void* S, void* Y, void* Z, int64_t rows, int64_t h, int64_t F,
                           tpmlp_activation act, cudaStream_t st) {
-    TPMLP_TRY((gemm_plain<T, float, EPI_F32>(K_F1, plain_args(rows, F, h, X, h, 1, A, F, 1, prod), nullptr, st)));
-    TPMLP_TRY(timed(K_C8, 0.0, (4.0 + 33.0 / 32.0 + sizeof(T)) * rows * F, st, [&] {
-        return act == TPMLP_GELU_TANH ? ckpt8_encode_launch<float, T, 2>(prod, a, Y, C, S, rows, F, st)
-                                      : ckpt8_encode_launch<float, T, 1>(prod, a, Y, C, S, rows, F, st);
-    }));
-    SimtArgs s2 = plain_args(rows, h, F, Y, F, 1, B, h, 1, Z);
-    s2.bias = b;
-    return gemm_plain<T, T, EPI_ADD>(K_F2, s2, static_cast<const T*>(R), st);
+    TiledProduct p1 = plain_args(rows, F, h, X, h, 1, A, F, 1, Y);
+    p1.a.bias = a;
+    set_c8(p1, C, S, F);
+    TPMLP_TRY((act == TPMLP_GELU_TANH ? gemm_plain<T, T, EPI_GELU_C8_TANH>(K_F1, p1, st)
+                                      : gemm_plain<T, T, EPI_GELU_C8>(K_F1, p1, st)));
+    TiledProduct p2 = plain_args(rows, h, F, Y, F, 1, B, h, 1, Z);
+    p2.a.bias = b;
+    p2.resid = R;
+    return gemm_plain<T, T, EPI_ADD>(K_F2, p2, st);
 }
 
 template <int EPI, typename TG>
@@ -634,27 +650,26 @@ tpmlp_status c8_bwd_tc(const Plan& pl, const void* dZ, const void* X, const void
 
 template <typename T, typename TG>
 tpmlp_status c8_bwd_plain(const Plan& pl, const void* dZ, const void* X, const void* A, const void* B, const void* C,
-                          const void* S, void* dX, TG* dA, TG* da, TG* dB, TG* db, void* dH, void* Y, float* prod,
-                          int64_t rows, int64_t h, int64_t F, tpmlp_activation act, void* workspace,
-                          cudaStream_t st) {
+                          const void* S, void* dX, TG* dA, TG* da, TG* dB, TG* db, void* dH, void* Y, int64_t rows,
+                          int64_t h, int64_t F, tpmlp_activation act, void* workspace, cudaStream_t st) {
     float* cs_h = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.off_cs_h);
     float* cs_f = reinterpret_cast<float*>(static_cast<char*>(workspace) + pl.off_cs_f);
-    TPMLP_TRY((gemm_plain<T, float, EPI_F32>(K_B2, plain_args(rows, F, h, dZ, h, 1, B, 1, h, prod), nullptr, st)));
-    TPMLP_TRY(timed(K_C8, 0.0, (4.0 + 33.0 / 32.0 + 2.0 * sizeof(T)) * rows * F, st, [&] {
-        return act == TPMLP_GELU_TANH ? ckpt8_decode_launch<T, 2>(C, S, prod, dH, Y, rows, F, st)
-                                      : ckpt8_decode_launch<T, 1>(C, S, prod, dH, Y, rows, F, st);
-    }));
+    TiledProduct p2 = plain_args(rows, F, h, dZ, h, 1, B, 1, h, dH);
+    p2.a.out1 = Y;
+    set_c8(p2, C, S, F);
+    TPMLP_TRY((act == TPMLP_GELU_TANH ? gemm_plain<T, T, EPI_DGELU_C8_TANH>(K_B2, p2, st)
+                                      : gemm_plain<T, T, EPI_DGELU_C8>(K_B2, p2, st)));
     TPMLP_TRY(colsum2(K_B12, static_cast<const T*>(dZ), h, cs_h, db, static_cast<const T*>(dH), F, cs_f, da, rows,
                       pl.chunks, st));
-    TPMLP_TRY((gemm_plain<T, TG, EPI_F32>(K_B3, plain_args(F, h, rows, Y, 1, F, dZ, h, 1, dB), nullptr, st)));
-    TPMLP_TRY((gemm_plain<T, TG, EPI_F32>(K_B4, plain_args(h, F, rows, X, 1, h, dH, F, 1, dA), nullptr, st)));
-    return gemm_plain<T, T, EPI_F32>(K_B5, plain_args(rows, h, F, dH, F, 1, A, 1, F, dX), nullptr, st);
+    const TiledProduct p4 = plain_args(h, F, rows, X, 1, h, dH, F, 1, dA);
+    TPMLP_TRY((gemm_plain<T, TG, EPI_F32>(K_B34, plain_args(F, h, rows, Y, 1, F, dZ, h, 1, dB), st, &p4)));
+    return gemm_plain<T, T, EPI_F32>(K_B5, plain_args(rows, h, F, dH, F, 1, A, 1, F, dX), st);
 }
 
 template <typename TG>
 tpmlp_status c8_bwd_typed(const Plan& pl, const void* dZ, const void* X, const void* A, const void* B, const void* C,
                           const void* S, void* dX, void* dA, void* da, void* dB, void* db, void* dH, void* Y,
-                          float* prod, int64_t T, int64_t h, int64_t F, tpmlp_dtype dt, tpmlp_activation act,
+                          int64_t T, int64_t h, int64_t F, tpmlp_dtype dt, tpmlp_activation act,
                           void* workspace, cudaStream_t st) {
     TG *gA = static_cast<TG*>(dA), *ga = static_cast<TG*>(da), *gB = static_cast<TG*>(dB),
        *gb = static_cast<TG*>(db);
@@ -667,10 +682,10 @@ tpmlp_status c8_bwd_typed(const Plan& pl, const void* dZ, const void* X, const v
     }
     if constexpr (sizeof(TG) == 4) {
         if (dt == TPMLP_FP32)
-            return c8_bwd_plain<float, TG>(pl, dZ, X, A, B, C, S, dX, gA, ga, gB, gb, dH, Y, prod, T, h, F, act,
+            return c8_bwd_plain<float, TG>(pl, dZ, X, A, B, C, S, dX, gA, ga, gB, gb, dH, Y, T, h, F, act,
                                            workspace, st);
     }
-    return c8_bwd_plain<bf16, TG>(pl, dZ, X, A, B, C, S, dX, gA, ga, gB, gb, dH, Y, prod, T, h, F, act, workspace,
+    return c8_bwd_plain<bf16, TG>(pl, dZ, X, A, B, C, S, dX, gA, ga, gB, gb, dH, Y, T, h, F, act, workspace,
                                   st);
 }
 
@@ -760,7 +775,8 @@ tpmlp_status tp_linear_bwd_ex(const void* dY, const void* X, const void* W, cons
                               static_cast<const void*>(dbias), static_cast<const void*>(dH)})
             if (q && !aligned16(q)) return TPMLP_ERR_ALIGN;
     }
-    if (!plain_grid_ok(N) || !plain_grid_ok(K)) return TPMLP_ERR_UNSUPPORTED;
+    if (!columns_ok(N) || !plain_grid_ok(K, N) || !plain_grid_ok(T, K) || pl.chunks > kMaxGridY)
+        return TPMLP_ERR_UNSUPPORTED;
     if (dt == TPMLP_FP32)
         return linear_bwd_ex_run<float, float>(pl, dY, X, W, H, dX, dW, dbias, dH, T, K, N, act, workspace, st);
     if (grad_dt == TPMLP_BF16)
@@ -769,10 +785,7 @@ tpmlp_status tp_linear_bwd_ex(const void* dY, const void* X, const void* W, cons
 }
 
 size_t tpmlp_ckpt8_workspace_size(int64_t T, int64_t h, int64_t F, int p, tpmlp_dtype dt) {
-    Plan pl;
-    size_t off = 0, total = 0;
-    if (!make_c8_plan(T, h, F, p, dt, &pl, &off, &total)) return 0;
-    return total;
+    return tpmlp_workspace_size(T, h, F, p, dt);
 }
 
 tpmlp_status tp_mlp_fwd_ckpt8(const void* X, const void* A, const void* a, const void* B, const void* b,
@@ -781,8 +794,7 @@ tpmlp_status tp_mlp_fwd_ckpt8(const void* X, const void* A, const void* a, const
                               void* stream) {
     cudaGetLastError();
     Plan pl;
-    size_t off = 0;
-    TPMLP_TRY(c8_checks(T, h, F, p, dt, act, &pl, &off, workspace, workspace_bytes));
+    TPMLP_TRY(c8_checks(T, h, F, p, dt, act, &pl, workspace, workspace_bytes));
     if (T == 0) return TPMLP_OK;
     if (!X || !A || !B || !C || !S || !Y || !Z) return TPMLP_ERR_INVALID;
     if (!aligned16(C)) return TPMLP_ERR_ALIGN;
@@ -794,9 +806,8 @@ tpmlp_status tp_mlp_fwd_ckpt8(const void* X, const void* A, const void* a, const
             return c8_fwd_tc<EPI_GELU_C8_TANH>(pl, X, A, a, B, b, R, C, S, Y, Z, T, h, F, workspace, st);
         return c8_fwd_tc<EPI_GELU_C8>(pl, X, A, a, B, b, R, C, S, Y, Z, T, h, F, workspace, st);
     }
-    float* prod = reinterpret_cast<float*>(static_cast<char*>(workspace) + off);
-    if (dt == TPMLP_FP32) return c8_fwd_plain<float>(X, A, a, B, b, R, C, S, Y, Z, prod, T, h, F, act, st);
-    return c8_fwd_plain<bf16>(X, A, a, B, b, R, C, S, Y, Z, prod, T, h, F, act, st);
+    if (dt == TPMLP_FP32) return c8_fwd_plain<float>(X, A, a, B, b, R, C, S, Y, Z, T, h, F, act, st);
+    return c8_fwd_plain<bf16>(X, A, a, B, b, R, C, S, Y, Z, T, h, F, act, st);
 }
 
 tpmlp_status tp_mlp_bwd_ckpt8(const void* dZ, const void* X, const void* A, const void* B, const void* C,
@@ -805,8 +816,7 @@ tpmlp_status tp_mlp_bwd_ckpt8(const void* dZ, const void* X, const void* A, cons
                               tpmlp_activation act, void* workspace, size_t workspace_bytes, void* stream) {
     cudaGetLastError();
     Plan pl;
-    size_t off = 0;
-    TPMLP_TRY(c8_checks(T, h, F, p, dt, act, &pl, &off, workspace, workspace_bytes));
+    TPMLP_TRY(c8_checks(T, h, F, p, dt, act, &pl, workspace, workspace_bytes));
     if (!known_grad(grad_dt, dt) || !dA || !da || !dB || !db) return TPMLP_ERR_INVALID;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (T == 0) {
@@ -824,11 +834,10 @@ tpmlp_status tp_mlp_bwd_ckpt8(const void* dZ, const void* X, const void* A, cons
                               static_cast<const void*>(Y)})
             if (!aligned16(q)) return TPMLP_ERR_ALIGN;
     }
-    float* prod = reinterpret_cast<float*>(static_cast<char*>(workspace) + off);
     if (grad_dt == TPMLP_BF16)
-        return c8_bwd_typed<bf16>(pl, dZ, X, A, B, C, S, dX, dA, da, dB, db, dH, Y, prod, T, h, F, dt, act,
+        return c8_bwd_typed<bf16>(pl, dZ, X, A, B, C, S, dX, dA, da, dB, db, dH, Y, T, h, F, dt, act,
                                   workspace, st);
-    return c8_bwd_typed<float>(pl, dZ, X, A, B, C, S, dX, dA, da, dB, db, dH, Y, prod, T, h, F, dt, act, workspace,
+    return c8_bwd_typed<float>(pl, dZ, X, A, B, C, S, dX, dA, da, dB, db, dH, Y, T, h, F, dt, act, workspace,
                                st);
 }
 
@@ -836,15 +845,15 @@ tpmlp_status tpmlp_ckpt8_encode(const void* H, void* C, void* S, int64_t T, int6
                                 void* stream) {
     cudaGetLastError();
     if (T < 0 || F < 1 || !known_dtype(dt) || (T > 0 && (!H || !C || !S))) return TPMLP_ERR_INVALID;
-    if (!fits32(T) || !fits32(F) || !plain_grid_ok(F)) return TPMLP_ERR_UNSUPPORTED;
+    if (!fits32(T) || !fits32(F) || !columns_ok(F)) return TPMLP_ERR_UNSUPPORTED;
     TPMLP_TRY(check_device());
     if (T == 0) return TPMLP_OK;
     if (!aligned16(C)) return TPMLP_ERR_ALIGN;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const double esize = dt == TPMLP_BF16 ? 2.0 : 4.0;
     return timed(K_C8, 0.0, (esize + 33.0 / 32.0) * T * F, st, [&] {
-        return dt == TPMLP_BF16 ? ckpt8_encode_launch<bf16, bf16, 0>(H, nullptr, nullptr, C, S, T, F, st)
-                                : ckpt8_encode_launch<float, float, 0>(H, nullptr, nullptr, C, S, T, F, st);
+        return dt == TPMLP_BF16 ? ckpt8_encode_launch<bf16>(H, C, S, T, F, st)
+                                : ckpt8_encode_launch<float>(H, C, S, T, F, st);
     });
 }
 
@@ -852,15 +861,15 @@ tpmlp_status tpmlp_ckpt8_decode(const void* C, const void* S, void* H, int64_t T
                                 void* stream) {
     cudaGetLastError();
     if (T < 0 || F < 1 || !known_dtype(dt) || (T > 0 && (!H || !C || !S))) return TPMLP_ERR_INVALID;
-    if (!fits32(T) || !fits32(F) || !plain_grid_ok(F)) return TPMLP_ERR_UNSUPPORTED;
+    if (!fits32(T) || !fits32(F) || !columns_ok(F)) return TPMLP_ERR_UNSUPPORTED;
     TPMLP_TRY(check_device());
     if (T == 0) return TPMLP_OK;
     if (!aligned16(C)) return TPMLP_ERR_ALIGN;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const double esize = dt == TPMLP_BF16 ? 2.0 : 4.0;
     return timed(K_C8, 0.0, (esize + 33.0 / 32.0) * T * F, st, [&] {
-        return dt == TPMLP_BF16 ? ckpt8_decode_launch<bf16, 0>(C, S, nullptr, H, nullptr, T, F, st)
-                                : ckpt8_decode_launch<float, 0>(C, S, nullptr, H, nullptr, T, F, st);
+        return dt == TPMLP_BF16 ? ckpt8_decode_launch<bf16>(C, S, H, T, F, st)
+                                : ckpt8_decode_launch<float>(C, S, H, T, F, st);
     });
 }
 

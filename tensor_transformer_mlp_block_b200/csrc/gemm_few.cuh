@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<TN>::CTAS)
         if (g.resid != nullptr && (lane & 15) == 0 && n0 + c < g.N) {
             // the residual's first touch of memory runs beside the product
             for (int t = rank; t < rows; t += S)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(g.resid + static_cast<int64_t>(t0 + t) * g.N + n0 + c));
+                prefetch_l2(g.resid + static_cast<int64_t>(t0 + t) * g.N + n0 + c);
         }
         // every lane waits and the warp goes on only together (.sync.aligned loads)
         ok = mbar_wait_bounded(smem_u32(done), 0, abort, limit);

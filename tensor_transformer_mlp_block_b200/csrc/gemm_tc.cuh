@@ -848,24 +848,37 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& g, const CUtensor
         // N hold zeros (their operand columns are read as zero, no bias).
         uint32_t codes[8];
         float c8s = 0.0f;
+        float hc8[EpiTraits<EPI>::kC8Out ? 32 : 1];
         if constexpr (EpiTraits<EPI>::kC8Out) {
-            float h[32];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 float bb[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                 if (g.bias != nullptr && col0 + 8 * q < N)
                     unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(g.bias + col0 + 8 * q)), bb);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) h[8 * q + i] = __uint_as_float(acc[8 * q + i]) + bb[i];
+                for (int i = 0; i < 8; ++i) hc8[8 * q + i] = __uint_as_float(acc[8 * q + i]) + bb[i];
             }
-            float top = 0.0f;
+            float top = fabsf(hc8[0]), top2 = fabsf(hc8[1]);  // two chains
 #pragma unroll
-            for (int i = 0; i < 32; ++i) top = max_nan(top, fabsf(h[i]));
-            const uint32_t sb = c8_scale_byte(top);
-            const float inv = c8_inverse(sb);
+            for (int i = 2; i < 32; i += 2) {
+                top = max_nan(top, fabsf(hc8[i]));
+                top2 = max_nan(top2, fabsf(hc8[i + 1]));
+            }
+            const uint32_t sb = c8_scale_byte(max_nan(top, top2));
+            const uint64_t inv2 = f2_splat(c8_inverse(sb));
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                codes[i] = sb == kC8NaN ? 0u : c8_pack4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3], inv);
+            for (int i = 0; i < 8; ++i) {
+                // c8_pack4 on packed pairs
+                const uint64_t round2 = f2_splat(kC8Round);
+                float t0, t1, t2, t3;
+                f2_unpack(f2_fma(f2_pack(hc8[4 * i], hc8[4 * i + 1]), inv2, round2), t0, t1);
+                f2_unpack(f2_fma(f2_pack(hc8[4 * i + 2], hc8[4 * i + 3]), inv2, round2), t2, t3);
+                codes[i] = c8_gather4(t0, t1, t2, t3);
+            }
+            if (sb == kC8NaN) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) codes[i] = 0u;
+            }
             if (row < M && col0 < N) {
                 uint4* dst = reinterpret_cast<uint4*>(g.c8 + static_cast<int64_t>(row) * g.c8_ld + col0);
                 dst[0] = make_uint4(codes[0], codes[1], codes[2], codes[3]);
@@ -891,7 +904,10 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& g, const CUtensor
             float v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(acc[8 * q + i]);
-            if constexpr (EpiTraits<EPI>::kBias) {
+            if constexpr (EpiTraits<EPI>::kC8Out) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[i] = hc8[8 * q + i];
+            } else if constexpr (EpiTraits<EPI>::kBias) {
                 if (g.bias != nullptr && c < N) {
                     float bb[8];
                     unpack_bf16x8(__ldg(reinterpret_cast<const uint4*>(g.bias + c)), bb);
@@ -1054,6 +1070,22 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& g, const CUtensorM
          ++local) {
         const int buf = local & 1;
         const uint32_t aphase = (local >> 1) & 1;
+        if constexpr (EpiTraits<EPI>::kResid || EpiTraits<EPI>::kC8In) {
+            // what the epilogue reads of this unit (its own 32 rows, half of the
+            // columns) is brought to L2 beside the main loop; the loads in the
+            // chunks then wait a fraction of what memory takes
+            const int64_t row = w.mb * tile_rows + cta_row_off + quad * 32 + lane;
+            const int col = w.nb * BN + half * (BN / 2);
+            if (row < g.M && col < g.N) {
+                if constexpr (EpiTraits<EPI>::kC8In) {
+                    prefetch_l2(g.c8 + row * g.c8_ld + col);
+                } else if (g.resid != nullptr) {
+#pragma unroll
+                    for (int c = 0; c < BN / 2; c += 64)
+                        if (col + c < g.N) prefetch_l2(g.resid + row * g.ld_out + col + c);
+                }
+            }
+        }
         // every lane waits; the warp proceeds only if all lanes saw the
         // phase complete, so the .sync.aligned loads below never diverge
         const bool ok = mbar_wait_bounded(smem_u32(&tfull[buf]), aphase, abort, limit);
