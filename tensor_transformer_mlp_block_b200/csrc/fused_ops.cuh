@@ -380,7 +380,9 @@ tpmlp_status gemm_few_launch(const void* X, const void* W, int T, int N, int K, 
 // against 35.3. A second tile would read W again.
 constexpr int64_t kFewMaxRows = 128;
 
-tpmlp_status linear_few(const void* X, const void* W, const void* bias, const void* R, void* H, void* Y, int T, int N,
+static_assert(kFewMaxRows >= kBM, "gemm_tc_pick relies on it");
+
+tpmlp_status linear_few(int kind, const void* X, const void* W, const void* bias, const void* R, void* H, void* Y, int T, int N,
                         int K, tpmlp_activation act, cudaStream_t st) {
     FewArgs g{};
     g.act = static_cast<int>(act);
@@ -389,7 +391,7 @@ tpmlp_status linear_few(const void* X, const void* W, const void* bias, const vo
     g.H = static_cast<bf16*>(H);
     g.Y = static_cast<bf16*>(Y);
     const double bytes = 2.0 * (double(T) * K + double(K) * N + (1.0 + (R != nullptr) + (H != nullptr)) * T * N);
-    return timed(K_L_FWD, 2.0 * T * N * K, bytes, st, [&] {
+    return timed(kind, 2.0 * T * N * K, bytes, st, [&] {
         if (T <= 16) return gemm_few_launch<16>(X, W, T, N, K, g, st);
         if (T <= 32) return gemm_few_launch<32>(X, W, T, N, K, g, st);
         if (T <= 64) return gemm_few_launch<64>(X, W, T, N, K, g, st);
@@ -427,7 +429,7 @@ tpmlp_status linear_fwd_ex_impl(const void* X, const void* W, const void* bias, 
     if (pl.tc) {
         for (const void* q : {X, W, bias, R, static_cast<const void*>(H), static_cast<const void*>(Y)})
             if (q && !aligned16(q)) return TPMLP_ERR_ALIGN;
-        if (T <= kFewMaxRows) return linear_few(X, W, bias, R, H, Y, iT, iN, iK, act, st);
+        if (T <= kFewMaxRows) return linear_few(K_L_FWD, X, W, bias, R, H, Y, iT, iN, iK, act, st);
         // the relaying activation epilogues run whole tiles (kSplittable)
         const SchedReq req = (act != TPMLP_ACT_NONE && K >= kRelayMinKAct) ? SchedReq{} : pl.fwd;
         GemmArgs g{};
@@ -562,6 +564,7 @@ tpmlp_status c8_fwd_tc(const Plan& pl, const void* X, const void* A, const void*
     g1.c8_scale = static_cast<uint8_t*>(S);
     g1.c8_ld = c8_blocks(F) * kC8Block;
     TPMLP_TRY((gemm_tc<256, false, true, EPI>(K_F1, X, A, iT, iF, ih, pl.f1, g1, st)));
+    if (T <= kFewMaxRows) return linear_few(K_F2, Y, B, b, R, nullptr, Z, iT, ih, iF, TPMLP_ACT_NONE, st);
     GemmArgs g2{};
     set_split_space(g2, workspace, pl.off_part, pl.off_ctr);
     g2.dyn_counter = dyn_space(workspace, pl.off_dyn);

@@ -54,7 +54,7 @@ enum EpiKind : int {
     EPI_GELU_ADD = 9,        // out0 = H = acc + bias, out1 = GeLU(H) + resid
     EPI_GELU_ADD_TANH = 10,
     // the 8-bit checkpoint (ckpt8.cuh): H in 8 bits between the passes
-    EPI_GELU_C8 = 11,        // c8 = H = acc + bias in 8 bits, out0 = Y = GeLU(H)
+    EPI_GELU_C8 = 11,        // out1 = c8 = H = acc + bias in 8 bits, out0 = Y = GeLU(H)
     EPI_GELU_C8_TANH = 12,
     EPI_DGELU_C8 = 13,       // out0 = dH = acc · GeLU′(H̃), out1 = Y = GeLU(H̃), H̃ from c8
     EPI_DGELU_C8_TANH = 14,
@@ -76,7 +76,10 @@ struct EpiTraits {
     static constexpr bool kResid = (EPI == EPI_ADD || EPI == EPI_ACT_ADD || EPI == EPI_ACT_ADD_TANH ||
                                     EPI == EPI_GELU_ADD || EPI == EPI_GELU_ADD_TANH);
     static constexpr bool kBias = (EPI == EPI_BIAS || EPI == EPI_ADD) || kAct || kActOnly;
-    static constexpr bool kTwo = kAct || kC8In;  // two outputs stored through the tensor maps
+    static constexpr bool kTwo = kAct || kC8In || kC8Out;  // two outputs stored through the tensor maps
+    // the residual's chunks come by TMA, through the half of the staging slot
+    // that a single output leaves free (its map travels as the second output's)
+    static constexpr bool kResidTma = kResid && !kAct;
     // the epilogue evaluates the activation or its derivative (its relay has no split path)
     static constexpr bool kMath = kAct || kDAct || kActOnly;
 };
@@ -101,8 +104,9 @@ struct GemmArgs {
     const __nv_bfloat16* bias;
     const __nv_bfloat16* aux;
     const __nv_bfloat16* resid;  // kResid epilogues: M × N, row stride ld_out; may be null, may be the output
-    // 8-bit checkpoint (kC8Out writes it, kC8In reads it): M rows of c8_ld bytes
-    // (a multiple of 32), and the scale bytes, one row of M per 32 columns
+    // 8-bit checkpoint (kC8Out writes it, through the second output's map; kC8In
+    // reads it): M rows of c8_ld bytes (a multiple of 32), and the scale bytes,
+    // one row of M per 32 columns
     uint8_t* c8;
     uint8_t* c8_scale;
     int64_t c8_ld;
@@ -153,7 +157,7 @@ struct TileCfg {
     static constexpr int STAGES = (196608 / STAGE_BYTES) > 8 ? 8 : (196608 / STAGE_BYTES);
     // tensor-memory columns: two accumulators, rounded up to a power of two
     static constexpr int TMEM_COLS = (2 * BN <= 128) ? 128 : (2 * BN <= 256 ? 256 : 512);
-    static constexpr int BAR_BYTES = 8 * (2 * STAGES + 5 + 8) + 16;
+    static constexpr int BAR_BYTES = 8 * (2 * STAGES + 5 + 8) + 16 + 8 * kEpiWarps;  // the last: residual loads
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + kEpiStagingBytes + BAR_BYTES;
 };
 
@@ -795,6 +799,70 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4& v, float* f) {
     }
 }
 
+// What the epilogue reads of one 32 × 32 chunk besides the accumulator: the
+// lane's row of the residual (kResid with two outputs), or of the 8-bit
+// checkpoint, its codes in ex[0..1] and its scale byte in ex[2].x (kC8In). The
+// caller issues it a chunk ahead, since a warp's rows lie in 32 different lines
+// and the loads take long. The residual is read with ordinary loads: it may be
+// the output.
+template <int EPI>
+__device__ __forceinline__ void load_extra(const GemmArgs& g, int row, int col0, int M, int N,
+                                           uint4 (&ex)[4]) {
+    if constexpr (EpiTraits<EPI>::kResid && !EpiTraits<EPI>::kResidTma) {
+        const __nv_bfloat16* p = g.resid + static_cast<int64_t>(row) * g.ld_out + col0;
+        const bool in = g.resid != nullptr && row < M;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            ex[q] = make_uint4(0, 0, 0, 0);
+            if (in && col0 + 8 * q < N) ex[q] = *reinterpret_cast<const uint4*>(p + 8 * q);
+        }
+    } else if constexpr (EpiTraits<EPI>::kC8In) {
+        ex[0] = ex[1] = ex[2] = make_uint4(0, 0, 0, 0);
+        if (row < M && col0 < N) {
+            const uint4* src =
+                reinterpret_cast<const uint4*>(g.c8 + static_cast<int64_t>(row) * g.c8_ld + col0);
+            ex[0] = __ldg(src);
+            ex[1] = __ldg(src + 1);
+            ex[2].x = __ldg(g.c8_scale + static_cast<int64_t>(col0 / kC8Block) * M + row);
+        }
+    }
+}
+
+// The residual's chunks on their way into the second half of the warp's staging
+// slot (kResidTma): one load in flight at a time, issued when the previous chunk
+// has been read, so that it lands during that chunk's arithmetic. Loaded a lane
+// per row they cost 32 lines per instruction: 6144 × 4096 outputs, K = 1024, bias
+// and residual took 78 µs on B200 that way, 55 issued a chunk ahead, against 41
+// without a residual.
+struct ResidLoad {
+    const CUtensorMap* map;
+    uint32_t bar, buf;
+    uint32_t phase;
+    bool on, in_flight;
+
+    __device__ __forceinline__ void issue(int row0, int col0, int lane) {
+        if (!on) return;
+        if (lane == 0) {
+            mbar_arrive_expect_tx(bar, 2048);
+            tma_load_2d(buf, map, bar, col0, row0);
+        }
+        in_flight = true;
+    }
+    // The lane's row of the chunk (zeros without a residual); false when the
+    // wait gave up. The buffer is free again afterwards.
+    __device__ __forceinline__ bool take(uint4 (&ex)[4], int lane, volatile int* abort, uint64_t limit) {
+        if (!on) return true;
+        const bool got = mbar_wait_bounded(bar, phase, abort, limit);
+        if (!__all_sync(0xffffffffu, got)) return false;
+        phase ^= 1u;
+        in_flight = false;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ex[q] = ld_shared_v4(buf + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4));
+        __syncwarp();
+        return true;
+    }
+};
+
 // Epilogue of one 32 × 32 chunk of the accumulator: this warp's 32 rows
 // row0 .. row0+31 (lane i holds row row0 + i) and columns col0 .. col0+31.
 // The results are written row by row into the warp's shared-memory staging
@@ -813,9 +881,11 @@ __device__ __forceinline__ void unpack_bf16x8(const uint4& v, float* f) {
 // cs_mode (GeLU′ epilogues with colsum_out): 0 = none; 1 = keep this chunk's
 // stored values in csx; 2 = add them to csx, reduce csx over the 32 lanes
 // and write the column sums to colsum_out row cs_row (if cs_row ≥ 0).
+// ex: what load_extra read for the chunk.
 template <int EPI, bool DBL>
 __device__ __forceinline__ void epilogue_chunk(const GemmArgs& g, const CUtensorMap* tmO0,
-                                               const CUtensorMap* tmO1, const uint32_t (&acc)[32],
+                                               const CUtensorMap* tmO1, const uint4 (&ex)[4],
+                                               const uint32_t (&acc)[32],
                                                int row0, int col0, int M, int N, uint32_t slot_base,
                                                uint32_t& sbuf, int lane, float (&csx)[32],
                                                int cs_mode, int64_t cs_row) {
@@ -879,24 +949,14 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& g, const CUtensor
 #pragma unroll
                 for (int i = 0; i < 8; ++i) codes[i] = 0u;
             }
-            if (row < M && col0 < N) {
-                uint4* dst = reinterpret_cast<uint4*>(g.c8 + static_cast<int64_t>(row) * g.c8_ld + col0);
-                dst[0] = make_uint4(codes[0], codes[1], codes[2], codes[3]);
-                dst[1] = make_uint4(codes[4], codes[5], codes[6], codes[7]);
+            // 32 consecutive bytes of the scales' row
+            if (row < M && col0 < N)
                 g.c8_scale[static_cast<int64_t>(col0 / kC8Block) * M + row] = static_cast<uint8_t>(sb);
-            }
         }
         if constexpr (EpiTraits<EPI>::kC8In) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) codes[i] = 0u;
-            if (row < M && col0 < N) {
-                const uint4* src =
-                    reinterpret_cast<const uint4*>(g.c8 + static_cast<int64_t>(row) * g.c8_ld + col0);
-                const uint4 a = __ldg(src), b = __ldg(src + 1);
-                codes[0] = a.x; codes[1] = a.y; codes[2] = a.z; codes[3] = a.w;
-                codes[4] = b.x; codes[5] = b.y; codes[6] = b.z; codes[7] = b.w;
-                c8s = c8_scale(__ldg(g.c8_scale + static_cast<int64_t>(col0 / kC8Block) * M + row));
-            }
+            codes[0] = ex[0].x; codes[1] = ex[0].y; codes[2] = ex[0].z; codes[3] = ex[0].w;
+            codes[4] = ex[1].x; codes[5] = ex[1].y; codes[6] = ex[1].z; codes[7] = ex[1].w;
+            c8s = c8_scale(ex[2].x);
         }
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -940,11 +1000,14 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& g, const CUtensor
                     f2_unpack(f2_mul(f2_pack(v[i], v[i + 1]), f2_pack(d0, d1)), v[i], v[i + 1]);
                 }
             }
-            float res[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+            float res[8];
             if constexpr (EpiTraits<EPI>::kResid) {
-                // an ordinary load: resid may be the output this kernel writes
-                if (g.resid != nullptr && row < M && c < N)
-                    unpack_bf16x8(*reinterpret_cast<const uint4*>(g.resid + off + 8 * q), res);
+                if (g.resid != nullptr) {
+                    unpack_bf16x8(ex[q], res);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) res[i] = 0.0f;
+                }
             }
             if constexpr (EpiTraits<EPI>::kActOnly) {
 #pragma unroll
@@ -981,7 +1044,12 @@ __device__ __forceinline__ void epilogue_chunk(const GemmArgs& g, const CUtensor
         for (int q = 0; q < 4; ++q) {
             const uint32_t a = lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
             st_shared_v4(slot + a, o0[q]);
-            if constexpr (EpiTraits<EPI>::kTwo) st_shared_v4(slot + 2048 + a, o1[q]);
+            if constexpr (EpiTraits<EPI>::kTwo && !EpiTraits<EPI>::kC8Out) st_shared_v4(slot + 2048 + a, o1[q]);
+        }
+        if constexpr (EpiTraits<EPI>::kC8Out) {
+            // the codes' 32-byte rows, unswizzled
+            st_shared_v4(slot + 2048 + lane * 32, make_uint4(codes[0], codes[1], codes[2], codes[3]));
+            st_shared_v4(slot + 2048 + lane * 32 + 16, make_uint4(codes[4], codes[5], codes[6], codes[7]));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -1044,7 +1112,8 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& g, const CUtensorM
                                               uint64_t* xempty, uint8_t* sEpi, int worker,
                                               int nworkers, int tile_rows, int cta_row_off,
                                               volatile int* abort, uint64_t limit, int warp,
-                                              int lane, const PairQueue* queue = nullptr) {
+                                              int lane, const PairQueue* queue = nullptr,
+                                              uint64_t* rbars = nullptr) {
     constexpr int kChunks = BN / 64;  // 32-column chunks per half of the tile
     const int quad = warp & 3;          // tensor-memory lanes this warp may access
     const int half = (warp - 2) / 4;    // which half of the tile's columns
@@ -1058,7 +1127,12 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& g, const CUtensorM
     const uint32_t partner_slot = smem_u32(sEpi + kSlotsPerWarp * (4 * half + quad) * kEpiSlotBytes);
     if (lane == 0 && !relay) {
         tma_prefetch_desc(tmO0);
-        if (EpiTraits<EPI>::kTwo || g.second) tma_prefetch_desc(tmO1);
+        if (EpiTraits<EPI>::kTwo || EpiTraits<EPI>::kResidTma || g.second) tma_prefetch_desc(tmO1);
+    }
+    ResidLoad resid{tmO1, 0u, slot + 2048, 0u, false, false};
+    if constexpr (EpiTraits<EPI>::kResidTma) {
+        resid.bar = smem_u32(&rbars[warp - 2]);
+        resid.on = g.resid != nullptr;
     }
     uint32_t xcount = 0;
     bool stored = false;  // a relay warp has bulk stores of a split tile in flight
@@ -1086,6 +1160,14 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& g, const CUtensorM
                 }
             }
         }
+        // the first chunk's residual (split tiles read theirs when they finish)
+        if constexpr (EpiTraits<EPI>::kResidTma)
+            if (w.pieces == 1 && !(RELAY && relay))
+                resid.issue(w.mb * tile_rows + cta_row_off + quad * 32, w.nb * BN + half * (BN / 2), lane);
+        uint4 next_ex[4];  // (not relayed) the next chunk's, from here the first one's
+        if constexpr (!RELAY && !EpiTraits<EPI>::kResidTma)
+            load_extra<EPI>(g, w.mb * tile_rows + cta_row_off + quad * 32 + lane, w.nb * BN + half * (BN / 2), g.M,
+                            g.N, next_ex);
         // every lane waits; the warp proceeds only if all lanes saw the
         // phase complete, so the .sync.aligned loads below never diverge
         const bool ok = mbar_wait_bounded(smem_u32(&tfull[buf]), aphase, abort, limit);
@@ -1154,14 +1236,31 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& g, const CUtensorM
                     }
                 }
                 float csx[32];  // unused: no column sums on split tiles
+                bool split_failed = false;
 #pragma unroll 1
                 for (int i = 0; i < kChunks; ++i) {
                     const int c = half * kChunks + i;
                     uint32_t acc[32];
+                    uint4 ex[4];
+                    if constexpr (EpiTraits<EPI>::kResidTma) {
+                        if (i == 0 || !resid.in_flight)
+                            resid.issue(tile_row0 + quad * 32, w.nb * BN + c * 32, lane);
+                        if (!resid.take(ex, lane, abort, limit)) {
+                            split_failed = true;
+                            break;
+                        }
+                        if (i + 1 < kChunks) resid.issue(tile_row0 + quad * 32, w.nb * BN + (c + 1) * 32, lane);
+                    } else {
+                        load_extra<EPI>(g, tile_row0 + quad * 32 + lane, w.nb * BN + c * 32, uM, uN, ex);
+                    }
                     partial_sum(g, w, nworkers, tile_rows, BN, own_r, c * 32, acc, lane,
                                 sure_last ? w.piece : -1, t_row + c * 32);
-                    epilogue_chunk<EPI, DBL>(g, uO, tmO1, acc, tile_row0 + quad * 32, w.nb * BN + c * 32,
+                    epilogue_chunk<EPI, DBL>(g, uO, tmO1, ex, acc, tile_row0 + quad * 32, w.nb * BN + c * 32,
                                              uM, uN, slot, sbuf, lane, csx, 0, -1);
+                }
+                if (split_failed) {
+                    raise_timeout(abort);
+                    break;
                 }
                 if (sure_last) {
                     // the accumulator was read in the loop above: release it, and
@@ -1200,6 +1299,24 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& g, const CUtensorM
             const int col0 = w.nb * BN + c * 32;
             uint32_t acc[32];
             tmem_ld_32x32b_x32(t_row + c * 32, acc);
+            uint4 ex[4];
+            if constexpr (EpiTraits<EPI>::kResidTma) {
+                if (!(RELAY && relay)) {
+                    if (!resid.take(ex, lane, abort, limit)) {
+                        failed = true;
+                        break;
+                    }
+                    if constexpr (RELAY) resid.issue(tile_row0 + (quad - 2) * 32, col0, lane);
+                    else if (i + 1 < kChunks) resid.issue(tile_row0 + quad * 32, col0 + 32, lane);
+                }
+            } else if constexpr (!RELAY) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) ex[q] = next_ex[q];
+                if (i + 1 < kChunks)
+                    load_extra<EPI>(g, tile_row0 + quad * 32 + lane, col0 + 32, uM, uN, next_ex);
+            } else if (!relay) {
+                load_extra<EPI>(g, tile_row0 + quad * 32 + lane, col0, uM, uN, ex);
+            }
             tmem_wait_ld();
             if (i == kChunks - 1) {
                 // this warp's part of the accumulator is in registers: release it
@@ -1227,9 +1344,18 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& g, const CUtensorM
                 ++xcount;
                 continue;
             }
-            epilogue_chunk<EPI, DBL>(g, uO, tmO1, acc, tile_row0 + quad * 32, col0, uM, uN, slot, sbuf,
+            epilogue_chunk<EPI, DBL>(g, uO, tmO1, ex, acc, tile_row0 + quad * 32, col0, uM, uN, slot, sbuf,
                                      lane, csx, cs_on ? 1 : 0, cs_row);
             if constexpr (RELAY) {
+                if constexpr (EpiTraits<EPI>::kResidTma) {
+                    if (!resid.take(ex, lane, abort, limit)) {
+                        failed = true;
+                        break;
+                    }
+                    if (i + 1 < kChunks) resid.issue(tile_row0 + quad * 32, col0 + 32, lane);
+                } else {
+                    load_extra<EPI>(g, tile_row0 + (quad - 2) * 32 + lane, col0, uM, uN, ex);
+                }
                 // the partner relay's chunk: same columns, rows of quad - 2
                 const bool got = mbar_wait_bounded(smem_u32(&xfull[pair_id]), xcount & 1u, abort, limit);
                 if (!__all_sync(0xffffffffu, got)) {
@@ -1247,7 +1373,7 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& g, const CUtensorM
                 }
                 mbar_arrive(smem_u32(&xempty[pair_id]));
                 ++xcount;
-                epilogue_chunk<EPI, DBL>(g, uO, tmO1, pacc, tile_row0 + (quad - 2) * 32, col0, uM, uN,
+                epilogue_chunk<EPI, DBL>(g, uO, tmO1, ex, pacc, tile_row0 + (quad - 2) * 32, col0, uM, uN,
                                          slot, sbuf, lane, csx, cs_on ? 2 : 0, cs_row);
             }
         }
@@ -1257,6 +1383,12 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& g, const CUtensorM
         }
     }
     if (!qok) raise_timeout(abort);
+    if constexpr (EpiTraits<EPI>::kResidTma) {
+        // wind down: a residual load still in flight
+        volatile int never = 0;
+        if (resid.in_flight) mbar_wait_bounded(resid.bar, resid.phase, &never, limit);
+        __syncwarp();
+    }
     if (lane == 0) bulk_wait0();  // this warp's stores are complete before exit
     __syncwarp();
 }
@@ -1293,11 +1425,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* xempty = bars + 2 * STAGES + 9;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 13);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
+    uint64_t* rbars = reinterpret_cast<uint64_t*>(tmem_slot + 4);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
+        if constexpr (EpiTraits<EPI>::kResidTma)
+            for (int x = 0; x < kEpiWarps; ++x) mbar_init(smem_u32(&rbars[x]), 1);
         for (int x = 0; x < 4; ++x) {
             mbar_init(smem_u32(&xfull[x]), 32);
             mbar_init(smem_u32(&xempty[x]), 32);
@@ -1466,7 +1601,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ------------------------------------------------ epilogue warps
         epilogue_role<BN, EPI, false, RELAY>(g, &tmO0, &tmO1, tmem_base, tfull, tempty, xfull, xempty, sEpi,
-                                             blockIdx.x, gridDim.x, kBM, 0, abort, limit, warp, lane);
+                                             blockIdx.x, gridDim.x, kBM, 0, abort, limit, warp, lane, nullptr,
+                                             rbars);
     }
 
     tc_fence_before();

@@ -35,8 +35,9 @@ struct Tile2Cfg {
     static constexpr int STAGING_BYTES = (DBL ? 2 : 1) * kEpiStagingBytes;
     static constexpr int TMEM_COLS = (2 * BN <= 256) ? 256 : 512;
     // barriers: ring (2·STAGES), accumulators (4), drain, relay (8), item
-    // queue (2·kQueue); then the TMEM address, the abort flag, the queue's items
-    static constexpr int BAR_BYTES = 8 * (2 * STAGES + 5 + 8 + 2 * kQueue) + 16 + 4 * kQueue;
+    // queue (2·kQueue); then the TMEM address, the abort flag, the queue's items,
+    // and the epilogue warps' residual loads
+    static constexpr int BAR_BYTES = 8 * (2 * STAGES + 5 + 8 + 2 * kQueue) + 16 + 4 * kQueue + 8 * kEpiWarps;
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + STAGING_BYTES + BAR_BYTES;
 };
 
@@ -77,6 +78,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(qempty + kQueue);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
     int* qitems = reinterpret_cast<int*>(tmem_slot + 4);
+    uint64_t* rbars = reinterpret_cast<uint64_t*>(qitems + kQueue);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -86,6 +88,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int npairs = static_cast<int>(num_clusters_x());
 
     if (threadIdx.x == 0) {
+        if constexpr (EpiTraits<EPI>::kResidTma)
+            for (int x = 0; x < kEpiWarps; ++x) mbar_init(smem_u32(&rbars[x]), 1);
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);
@@ -291,7 +295,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         // ------------------------------------------------ epilogue warps (both CTAs)
         epilogue_role<BN, EPI, true, RELAY, LONG>(g, &tmO0, &tmO1, tmem_base, tfull, tempty, xfull, xempty, sEpi,
                                             pair, npairs, kPairM, static_cast<int>(rank) * kBM, abort,
-                                            limit, warp, lane, dyn ? &queue : nullptr);
+                                            limit, warp, lane, dyn ? &queue : nullptr, rbars);
     }
 
     tc_fence_before();

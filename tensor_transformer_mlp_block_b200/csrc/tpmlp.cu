@@ -130,11 +130,41 @@ bool make_out_map(CUtensorMap* m, void* ptr, int64_t rows, int64_t cols, bool f3
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The 8-bit checkpoint's codes, rows of `ld` bytes (a multiple of 32), stored in
+// unswizzled 32 × 32 boxes.
+bool make_c8_map(CUtensorMap* m, void* ptr, int64_t rows, int64_t ld) {
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[3] = {static_cast<cuuint64_t>(ld), static_cast<cuuint64_t>(rows), 1};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld), static_cast<cuuint64_t>(rows) * static_cast<cuuint64_t>(ld)};
+    cuuint32_t box[3] = {32u, 32u, 1u};
+    cuuint32_t estr[3] = {1u, 1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, ptr, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// A residual (row-major bf16, M × N) read in 32 × 32 boxes in the layout the
+// epilogue stages its bf16 output in (64-byte rows, 64-byte swizzle).
+bool make_resid_map(CUtensorMap* m, const void* ptr, int64_t rows, int64_t cols) {
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+    cuuint32_t box[2] = {32u, 32u};
+    cuuint32_t estr[2] = {1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int EPI>
 bool make_out_maps(CUtensorMap* o0, CUtensorMap* o1, const GemmArgs& g, int M, int N) {
     const bool f32 = (EPI == EPI_F32);
     if (!make_out_map(o0, g.out0, M, N, f32)) return false;
+    if (EpiTraits<EPI>::kC8Out) return make_c8_map(o1, g.c8, M, g.c8_ld);
     if (EpiTraits<EPI>::kTwo) return make_out_map(o1, g.out1, M, N, false);
+    if (EpiTraits<EPI>::kResidTma && g.resid != nullptr) return make_resid_map(o1, g.resid, M, N);
     *o1 = *o0;
     return true;
 }
@@ -485,7 +515,9 @@ tpmlp_status gemm_tc_pick(const void* Aop, const void* Bop, int M, int N, int K,
         }
         return gemm_tc2_launch<BN, A_MN, B_MN, EPI, RELAY>(Aop, Bop, M, N, K, req, g, st);
     }
-    return gemm_tc_launch<BN, A_MN, B_MN, EPI, RELAY>(Aop, Bop, M, N, K, req, g, st);
+    // (the linear layer's epilogues never come here with so few rows: gemm_few.cuh)
+    if constexpr (EpiTraits<EPI>::kResid) return TPMLP_ERR_INVALID;
+    else return gemm_tc_launch<BN, A_MN, B_MN, EPI, RELAY>(Aop, Bop, M, N, K, req, g, st);
 }
 
 // Shortest K loop per work unit for which the relaying epilogue pays
