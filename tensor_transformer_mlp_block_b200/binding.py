@@ -524,6 +524,8 @@ def _give(t, name, shape, like, dtype=None):
     """An output: the caller's, checked, or a new one on like's device (dtype:
     like's if None)."""
     if t is None:
+        if like.shape == shape and (dtype is None or dtype is like.dtype):
+            return torch.empty_like(like)
         return like.new_empty(shape, dtype=dtype)
     _need(t, name, shape, like.dtype if dtype is None else dtype, like.device)
     return t
@@ -584,7 +586,7 @@ def layernorm_forward(X, gamma, beta, *, eps: float = 1e-5, stats: bool = True, 
         Y = _give(Y, "Y", (T, h), X)
         if stats:
             mean = _give(mean, "mean", (T,), X, torch.float32)
-            rstd = _give(rstd, "rstd", (T,), X, torch.float32)
+            rstd = _give(rstd, "rstd", (T,), mean)
         else:
             mean = rstd = None
         st = lib().tp_layernorm_fwd(px, pg, pb, Y.data_ptr(), _ptr(mean), _ptr(rstd), T, h, eps, code,
@@ -615,7 +617,7 @@ def layernorm_backward(dY, X, gamma, mean, rstd, *, residual_grad=None, out=None
         dX, dgamma, dbeta = (None, None, None) if out is None else out
         dX = _give(dX, "dX", (T, h), X)
         dgamma = _give(dgamma, "dgamma", (h,), X, f32)
-        dbeta = _give(dbeta, "dbeta", (h,), X, f32)
+        dbeta = _give(dbeta, "dbeta", (h,), dgamma)
         L = lib()
         ws, nb = _work(int(L.tpmlp_layernorm_workspace_size(T, h, code)), workspace, dev)
         st = L.tp_layernorm_bwd(py, px, pg, pm, pr, pd, dX.data_ptr(), dgamma.data_ptr(), dbeta.data_ptr(),
