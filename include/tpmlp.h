@@ -174,9 +174,11 @@ tpmlp_status tp_linear_bwd(const void* dY, const void* X, const void* W, void* d
  *   dW = Xᵀ·dH, dX = dH·Wᵀ   (from the stored dH)
  * With TPMLP_ACT_NONE, dH is dY: H and dH must be NULL. dW and dbias have the
  * type grad_dt: TPMLP_FP32, or dt for gradients held in the weights' type.
- * Both calls need tpmlp_linear_ex_workspace_size() bytes of workspace (the
- * larger of the two calls' needs; 0 for invalid sizes). With T == 0, dW and
- * dbias are set to zero. */
+ * The backward needs tpmlp_linear_ex_workspace_size() bytes of workspace (0
+ * for invalid sizes). The forward needs them only where its schedule splits
+ * tiles (never up to 128 rows, on the plain path or under split policy 1);
+ * without them it then returns TPMLP_ERR_WORKSPACE. With T == 0, dW and dbias
+ * are set to zero. */
 size_t tpmlp_linear_ex_workspace_size(int64_t T, int64_t K, int64_t N, int p, tpmlp_split split,
                                       tpmlp_dtype dt);
 tpmlp_status tp_linear_fwd_ex(const void* X, const void* W, const void* bias, const void* R, void* H,
@@ -263,8 +265,11 @@ tpmlp_status tp_mlp_recompute_hidden(const void* X, const void* A, const void* a
  * act′(H̃), Y = act(H̃) (rebuilt, written to Y, T×F), dB = Yᵀ·dZ, dA = Xᵀ·dH,
  * dX = Σ dH_i·A_iᵀ, da = 1ᵀ·dH, db = 1ᵀ·dZ. R's gradient is dZ itself.
  * Arguments as tp_mlp_bwd_ex; dA, da, dB and db have the type grad_dt:
- * TPMLP_FP32, or dt for gradients held in the weights' type. Both calls need
- * tpmlp_ckpt8_workspace_size() bytes (0 for invalid sizes).
+ * TPMLP_FP32, or dt for gradients held in the weights' type.
+ * The backward needs tpmlp_ckpt8_workspace_size() bytes (0 for invalid
+ * sizes). The forward needs them only where one of its products splits tiles
+ * or runs the dynamic schedule (see the two settings below); without them it
+ * then returns TPMLP_ERR_WORKSPACE.
  *
  * tpmlp_ckpt8_encode writes C and S of a T×F matrix H of dtype dt (for
  * other activations a caller keeps); tpmlp_ckpt8_decode writes the values C

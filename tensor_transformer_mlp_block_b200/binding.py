@@ -654,12 +654,16 @@ def fused_linear_forward(X, W, bias, p: int = 1, split: str = "columns", *, acti
     pb = _take(bias, "bias", (N,), dt, dev)
     pr = _take(residual, "residual", (T, N), dt, dev)
     with _scope(dev, stream):
-        Y = _give(out, "out", (T, N), X)
-        H = _give(hidden, "hidden", (T, N), X) if keep_hidden or hidden is not None else None
+        Y = _give(out, "out", (T, N), X if residual is None else residual)
+        H = _give(hidden, "hidden", (T, N), Y) if keep_hidden or hidden is not None else None
         L = lib()
-        ws, nb = _work(int(L.tpmlp_linear_ex_workspace_size(T, K, N, int(p), split_code, code)), workspace, dev)
-        st = L.tp_linear_fwd_ex(px, pw, pb, pr, _ptr(H), Y.data_ptr(), T, K, N, int(p), split_code, code, act,
-                                ws.data_ptr(), nb, _stream_of(dev))
+        args = (px, pw, pb, pr, _ptr(H), Y.data_ptr(), T, K, N, int(p), split_code, code, act)
+        if workspace is None:
+            # most calls need none: one that does says so before it launches anything
+            st = L.tp_linear_fwd_ex(*args, None, 0, _stream_of(dev))
+        if workspace is not None or st == ERR_WORKSPACE:
+            ws, nb = _work(int(L.tpmlp_linear_ex_workspace_size(T, K, N, int(p), split_code, code)), workspace, dev)
+            st = L.tp_linear_fwd_ex(*args, ws.data_ptr(), nb, _stream_of(dev))
     _check(st, "tp_linear_fwd_ex")
     return Y if H is None else (Y, H)
 
@@ -686,9 +690,9 @@ def fused_linear_backward(dY, X, W, H=None, p: int = 1, split: str = "columns", 
     with _scope(dev, stream):
         dX, dW, db, dH = (tuple(out or ()) + (None,) * 4)[:4]
         dX = _give(dX, "dX", (T, K), X)
-        dW = _give(dW, "dW", (K, N), X, grad_dtype)
+        dW = _give(dW, "dW", (K, N), W, grad_dtype)
         db = _give(db, "dbias", (N,), X, grad_dtype)
-        dH = None if H is None else _give(dH, "dH", (T, N), X)
+        dH = None if H is None else _give(dH, "dH", (T, N), H)
         L = lib()
         ws, nb = _work(int(L.tpmlp_linear_ex_workspace_size(T, K, N, int(p), split_code, code)), workspace, dev)
         st = L.tp_linear_bwd_ex(py, px, pw, ph, dX.data_ptr(), dW.data_ptr(), db.data_ptr(), _ptr(dH), T, K, N,
@@ -769,10 +773,14 @@ def forward_ckpt8(X, A, a, B, b, p: int, *, residual=None, activation: str = "ge
         Z = _give(Z, "Z", (T, h), X)
         Y = _give(scratch, "scratch", (T, F), X)
         L = lib()
-        ws, nb = _work(int(L.tpmlp_ckpt8_workspace_size(T, h, F, int(p), code)), workspace, dev)
-        st = L.tp_mlp_fwd_ckpt8(px, pA, pa, pB, pb, pr, C.data_ptr(), S.data_ptr(), Y.data_ptr(), Z.data_ptr(),
-                                T, h, F, int(p), code, act, ws.data_ptr(), nb,
-                                _stream_of(dev))
+        args = (px, pA, pa, pB, pb, pr, C.data_ptr(), S.data_ptr(), Y.data_ptr(), Z.data_ptr(), T, h, F, int(p),
+                code, act)
+        if workspace is None:
+            # most calls need none: one that does says so before it launches anything
+            st = L.tp_mlp_fwd_ckpt8(*args, None, 0, _stream_of(dev))
+        if workspace is not None or st == ERR_WORKSPACE:
+            ws, nb = _work(int(L.tpmlp_ckpt8_workspace_size(T, h, F, int(p), code)), workspace, dev)
+            st = L.tp_mlp_fwd_ckpt8(*args, ws.data_ptr(), nb, _stream_of(dev))
     _check(st, "tp_mlp_fwd_ckpt8")
     return C, S, Z
 
@@ -797,10 +805,12 @@ def backward_ckpt8(dZ, X, A, B, C, S, p: int, *, activation: str = "gelu", grad_
     ps = _take(S, "S", ss, torch.uint8, dev)
     with _scope(dev, stream):
         given = out or {}
-        res = {name: _give(given.get(name), name, shp, X, d)
-               for name, shp, d in (("dX", (T, h), dt), ("dA", (h, F), grad_dtype), ("da", (F,), grad_dtype),
-                                    ("dB", (F, h), grad_dtype), ("db", (h,), grad_dtype), ("dH", (T, F), dt),
-                                    ("Y", (T, F), dt))}
+        dH = _give(given.get("dH"), "dH", (T, F), X)
+        res = dict(dX=_give(given.get("dX"), "dX", (T, h), X), dA=_give(given.get("dA"), "dA", (h, F), A, grad_dtype),
+                   da=_give(given.get("da"), "da", (F,), X, grad_dtype),
+                   dB=_give(given.get("dB"), "dB", (F, h), B, grad_dtype),
+                   db=_give(given.get("db"), "db", (h,), X, grad_dtype), dH=dH,
+                   Y=_give(given.get("Y"), "Y", (T, F), dH))
         L = lib()
         ws, nb = _work(int(L.tpmlp_ckpt8_workspace_size(T, h, F, int(p), code)), workspace, dev)
         st = L.tp_mlp_bwd_ckpt8(pz, px, pA, pB, pc, ps, res["dX"].data_ptr(), res["dA"].data_ptr(),

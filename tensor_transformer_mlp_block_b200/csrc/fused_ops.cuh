@@ -420,21 +420,23 @@ tpmlp_status linear_fwd_ex_impl(const void* X, const void* W, const void* bias, 
                                 tpmlp_activation act, void* workspace, size_t workspace_bytes,
                                 cudaStream_t st) {
     LinPlan pl;
-    TPMLP_TRY(lin_checks(T, K, N, p, split, dt, &pl, workspace, workspace_bytes));
+    TPMLP_TRY(lin_checks(T, K, N, p, split, dt, &pl, workspace, workspace_bytes, false));
     if (act != TPMLP_ACT_NONE && !known_act(act)) return TPMLP_ERR_INVALID;
     if (act == TPMLP_ACT_NONE && H != nullptr) return TPMLP_ERR_INVALID;
     if (T == 0) return TPMLP_OK;
     if (!X || !W || !Y) return TPMLP_ERR_INVALID;
+    // the relaying activation epilogues run whole tiles (kSplittable)
+    const SchedReq req = (act != TPMLP_ACT_NONE && K >= kRelayMinKAct) ? SchedReq{} : pl.fwd;
+    const bool splits = pl.tc && T > kFewMaxRows && req.kind != SCHED_TILES;
+    if (splits && (workspace == nullptr || workspace_bytes < pl.total)) return TPMLP_ERR_WORKSPACE;
     const int iT = static_cast<int>(T), iK = static_cast<int>(K), iN = static_cast<int>(N);
     if (pl.tc) {
         for (const void* q : {X, W, bias, R, static_cast<const void*>(H), static_cast<const void*>(Y)})
             if (q && !aligned16(q)) return TPMLP_ERR_ALIGN;
         if (T <= kFewMaxRows) return linear_few(K_L_FWD, X, W, bias, R, H, Y, iT, iN, iK, act, st);
-        // the relaying activation epilogues run whole tiles (kSplittable)
-        const SchedReq req = (act != TPMLP_ACT_NONE && K >= kRelayMinKAct) ? SchedReq{} : pl.fwd;
         GemmArgs g{};
-        set_split_space(g, workspace, pl.off_part, pl.off_ctr);
-        if (req.kind != SCHED_TILES) TPMLP_TRY(reset_counters(workspace, pl.off_ctr, pl.ctr_bytes, st));
+        if (splits) set_split_space(g, workspace, pl.off_part, pl.off_ctr);
+        if (splits) TPMLP_TRY(reset_counters(workspace, pl.off_ctr, pl.ctr_bytes, st));
         g.out0 = H != nullptr ? H : Y;
         g.out1 = Y;
         g.ld_out = N;
@@ -551,9 +553,9 @@ tpmlp_status ckpt8_decode_launch(const void* C, const void* S, void* H, int64_t 
 }
 
 tpmlp_status c8_checks(int64_t T, int64_t h, int64_t F, int p, tpmlp_dtype dt, tpmlp_activation act, Plan* pl,
-                       void* ws, size_t ws_bytes) {
+                       void* ws, size_t ws_bytes, bool need_ws) {
     if (!known_act(act)) return TPMLP_ERR_INVALID;
-    TPMLP_TRY(common_checks(T, h, F, p, dt, pl, ws, ws_bytes));
+    TPMLP_TRY(common_checks(T, h, F, p, dt, pl, ws, ws_bytes, need_ws));
     if (!plain_grid_ok(T, F) || !plain_grid_ok(T, h) || !plain_grid_ok(h, F) || pl->chunks > kMaxGridY)
         return TPMLP_ERR_UNSUPPORTED;
     return TPMLP_OK;
@@ -564,9 +566,12 @@ tpmlp_status c8_fwd_tc(const Plan& pl, const void* X, const void* A, const void*
                        const void* R, void* C, void* S, void* Y, void* Z, int64_t T, int64_t h, int64_t F,
                        void* workspace, cudaStream_t st) {
     const int iT = static_cast<int>(T), ih = static_cast<int>(h), iF = static_cast<int>(F);
+    // (a workspace is there only if some product splits or runs dynamically)
     GemmArgs g1{};
-    set_split_space(g1, workspace, pl.off_part, pl.off_ctr);
-    g1.dyn_counter = dyn_space(workspace, pl.off_dyn);
+    if (workspace != nullptr) {
+        set_split_space(g1, workspace, pl.off_part, pl.off_ctr);
+        g1.dyn_counter = dyn_space(workspace, pl.off_dyn);
+    }
     if (pl.fwd_dyn)
         TPMLP_TRY(reset_counters(workspace, pl.off_ctr, pl.ctr_bytes, st));
     else if (pl.fwd_split)
@@ -580,8 +585,10 @@ tpmlp_status c8_fwd_tc(const Plan& pl, const void* X, const void* A, const void*
     TPMLP_TRY((gemm_tc<256, false, true, EPI>(K_F1, X, A, iT, iF, ih, pl.f1, g1, st)));
     if (T <= kFewMaxRows) return linear_few(K_F2, Y, B, b, R, nullptr, Z, iT, ih, iF, TPMLP_ACT_NONE, st);
     GemmArgs g2{};
-    set_split_space(g2, workspace, pl.off_part, pl.off_ctr);
-    g2.dyn_counter = dyn_space(workspace, pl.off_dyn);
+    if (workspace != nullptr) {
+        set_split_space(g2, workspace, pl.off_part, pl.off_ctr);
+        g2.dyn_counter = dyn_space(workspace, pl.off_dyn);
+    }
     g2.out0 = Z;
     g2.ld_out = h;
     g2.bias = static_cast<const bf16*>(b);
@@ -812,9 +819,12 @@ tpmlp_status tp_mlp_fwd_ckpt8(const void* X, const void* A, const void* a, const
                               void* stream) {
     cudaGetLastError();
     Plan pl;
-    TPMLP_TRY(c8_checks(T, h, F, p, dt, act, &pl, workspace, workspace_bytes));
+    TPMLP_TRY(c8_checks(T, h, F, p, dt, act, &pl, workspace, workspace_bytes, false));
     if (T == 0) return TPMLP_OK;
     if (!X || !A || !B || !C || !S || !Y || !Z) return TPMLP_ERR_INVALID;
+    if ((pl.fwd_split || pl.fwd_dyn) && (workspace == nullptr || workspace_bytes < pl.total))
+        return TPMLP_ERR_WORKSPACE;
+    if (!pl.fwd_split && !pl.fwd_dyn) workspace = nullptr;
     if (!aligned16(C)) return TPMLP_ERR_ALIGN;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (pl.tc) {
@@ -834,7 +844,7 @@ tpmlp_status tp_mlp_bwd_ckpt8(const void* dZ, const void* X, const void* A, cons
                               tpmlp_activation act, void* workspace, size_t workspace_bytes, void* stream) {
     cudaGetLastError();
     Plan pl;
-    TPMLP_TRY(c8_checks(T, h, F, p, dt, act, &pl, workspace, workspace_bytes));
+    TPMLP_TRY(c8_checks(T, h, F, p, dt, act, &pl, workspace, workspace_bytes, true));
     if (!known_grad(grad_dt, dt) || !dA || !da || !dB || !db) return TPMLP_ERR_INVALID;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (T == 0) {

@@ -967,14 +967,14 @@ bool make_lin_plan(int64_t T, int64_t K, int64_t N, int p, int split, tpmlp_dtyp
 }
 
 tpmlp_status lin_checks(int64_t T, int64_t K, int64_t N, int p, int split, tpmlp_dtype dt,
-                        LinPlan* pl, void* ws, size_t ws_bytes) {
+                        LinPlan* pl, void* ws, size_t ws_bytes, bool need_ws = true) {
     if (!make_lin_plan(T, K, N, p, split, dt, pl)) return TPMLP_ERR_INVALID;
     if (T >= (int64_t(1) << 31) || K >= (int64_t(1) << 31) || N >= (int64_t(1) << 31))
         return TPMLP_ERR_UNSUPPORTED;
     const DeviceInfo* d = device_info();
     if (d == nullptr) return TPMLP_ERR_CUDA;
     if (d->cc_major != 10) return TPMLP_ERR_UNSUPPORTED;
-    if (pl->total > 0 && (ws == nullptr || ws_bytes < pl->total))
+    if (need_ws && pl->total > 0 && (ws == nullptr || ws_bytes < pl->total))
         return TPMLP_ERR_WORKSPACE;
     if (ws != nullptr && !aligned16(ws)) return TPMLP_ERR_ALIGN;
     return TPMLP_OK;
