@@ -215,14 +215,15 @@ __global__ void __launch_bounds__(256) ckpt8_decode_kernel(const uint8_t* __rest
 
 // --------------------------------------------------- plain path, tiled product
 // The CUDA-core product of simt.cuh with register tiles: BT × BT outputs per
-// block of 256 threads, TM × TM each (TM = BT/16), 16-deep k tiles in shared
-// memory, the next tile's global loads in flight during the current one's
-// arithmetic. Each output is an fp32 accumulator updated with fmaf over k in
-// ascending order; with S > 1 (BT = 64) a cluster of S blocks takes consecutive
-// parts of K, and each block adds the parts of its 64/S rows in ascending k
-// (few output tiles and a long K: weight gradients of narrow layers, single
-// tokens). A launch may hold a second product of the same kind, whose tiles
-// follow the first's.
+// block (64 or 128), 8 × BT/16 a thread as packed pairs of fp32 (two rows), and
+// 16-deep k tiles in shared memory. fp32 operands come through a ring of
+// asynchronous copies, 16 bytes where rows allow it; bf16 operands are converted
+// on the way, one tile ahead in registers. Each output is an fp32 accumulator
+// updated with fma over k in ascending order. SPLIT (BT = 64): a cluster of S
+// blocks takes consecutive parts of K, and each block adds the parts of its 64/S
+// rows in ascending k (few output tiles and a long K: weight gradients of narrow
+// layers, short batches). A launch may hold a second product of the same kind,
+// whose tiles follow the first's.
 struct TiledProduct {
     SimtArgs a;
     const void* resid;  // kResid: M × N of the operands' type, row stride ld_out; may be null
@@ -260,130 +261,231 @@ __device__ __forceinline__ void tiled_store(const TiledProduct& p, int64_t m, in
     }
 }
 
-template <typename TI, typename TO, int EPI, int BT>
-__global__ void __launch_bounds__(256) simt_tiled_kernel(const TiledProduct p0, const TiledProduct p1, int S) {
-    constexpr int TM = BT / 16, BK = 16, LD = BT + 4;
-    __shared__ float sA[2][BK][LD];
-    __shared__ float sB[2][BK][LD];
-    __shared__ float parts[BT == 64 ? 64 * 64 : 1];  // [rank][row of this block's][column]
+// One operand's part of a k tile: element (x, k), x the tile's row (or column),
+// at p[x·sx + k·sk]; one of the strides is 1. It lies in shared memory as [k][LD]
+// whichever it is, so that a thread's eight rows are pairs of registers as they
+// come from there (with [x][k] the packing costs more than the copies save:
+// 2048 × 1024, K = 1024 fp32 170-200 µs against 127-147). vec: x is the unit
+// stride and 16-byte copies of 4 elements are aligned.
+template <typename TI, int BT>
+struct TiledOperand {
+    static constexpr int BK = 16, LD = BT + 4, NT = BT == 128 ? 256 : 128;
+    static constexpr int PER = BT * BK / NT;
+    const TI* p;  // at the tile's first row
+    int64_t sx, sk;
+    int left;  // rows of the tile inside the matrix
+    bool k_unit, vec;
+
+    // element e of the tile: consecutive threads along the unit stride
+    __device__ __forceinline__ void place(int e, int& x, int& k) const {
+        x = k_unit ? e / BK : e % BT;
+        k = k_unit ? e % BK : e / BT;
+    }
+    // fp32: asynchronous copies of k tile k0 (up to kend) into s[k][x]
+    __device__ __forceinline__ void copy(float (*s)[LD], int k0, int kend, int t) const {
+        if (vec) {
+#pragma unroll
+            for (int i = 0; i < PER / 4; ++i) {
+                const int e = t + NT * i, x = e % (BT / 4) * 4, k = e / (BT / 4);
+                const int in = k0 + k < kend ? min(max(left - x, 0), 4) : 0;
+                cp_async16(smem_u32(&s[k][x]), in > 0 ? p + (k0 + k) * sk + x : p, 4 * in);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                int x, k;
+                place(t + NT * i, x, k);
+                const bool in = x < left && k0 + k < kend;
+                cp_async4(smem_u32(&s[k][x]), in ? p + x * sx + (k0 + k) * sk : p, in ? 4 : 0);
+            }
+        }
+    }
+    __device__ __forceinline__ void fetch(TI (&r)[PER], int k0, int kend, int t) const {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            int x, k;
+            place(t + NT * i, x, k);
+            r[i] = x < left && k0 + k < kend ? p[x * sx + (k0 + k) * sk] : from_f32<TI>(0.0f);
+        }
+    }
+    __device__ __forceinline__ void stash(float (*s)[LD], const TI (&r)[PER], int t) const {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            int x, k;
+            place(t + NT * i, x, k);
+            s[k][x] = to_f32<TI>(r[i]);
+        }
+    }
+};
+
+template <typename TI, int BT>
+__device__ __forceinline__ TiledOperand<TI, BT> tiled_operand(const void* base, int64_t sx, int64_t sk, int64_t x0,
+                                                              int extent) {
+    TiledOperand<TI, BT> o;
+    o.p = static_cast<const TI*>(base) + x0 * sx;
+    o.sx = sx;
+    o.sk = sk;
+    o.left = static_cast<int>(min(static_cast<int64_t>(BT), extent - x0));
+    o.k_unit = sk == 1;
+    o.vec = sx == 1 && sk % 4 == 0 && (reinterpret_cast<uintptr_t>(base) & 15u) == 0;
+    return o;
+}
+
+template <typename TI, typename TO, int EPI, int BT, bool SPLIT>
+__global__ void __launch_bounds__(BT == 128 ? 256 : 128, BT == 128 ? 2 : 4)
+    simt_tiled_kernel(const TiledProduct p0, const TiledProduct p1, int S) {
+    static_assert(BT == 64 || (BT == 128 && !SPLIT), "tiles of 64 (K may be split) or 128");
+    constexpr int BK = 16, LD = BT + 4, NT = BT == 128 ? 256 : 128, TN = BT / 16;
+    // fp32: tiles in flight and in use; bf16: the tile in use and the next one
+    constexpr int STAGES = sizeof(TI) == 4 && BT == 64 ? 4 : 2;
+    __shared__ __align__(16) float sA[STAGES][BK][LD];
+    __shared__ __align__(16) float sB[STAGES][BK][LD];
     const int tiles0 = p0.mb * p0.nb;
     const bool second = static_cast<int>(blockIdx.x) >= tiles0;
     const TiledProduct& p = second ? p1 : p0;
     const SimtArgs& g = p.a;
     const int tile = static_cast<int>(blockIdx.x) - (second ? tiles0 : 0);
     const int t = threadIdx.x;
-    const int tx = t & 15, ty = t >> 4;
+    const int tx = t % 16, ty = t / 16;  // rows 4·ty.. and BT/2 + 4·ty..; columns 4·tx.. (and 64 + 4·tx..)
+    auto column = [&](int j) { return 16 * (j & ~3) + 4 * tx + (j & 3); };
     const int64_t m0 = static_cast<int64_t>(tile % p.mb) * BT, n0 = static_cast<int64_t>(tile / p.mb) * BT;
-    const int rank = static_cast<int>(blockIdx.z);
+    const int rank = SPLIT ? static_cast<int>(blockIdx.z) : 0;
     const int steps = (g.K + BK - 1) / BK;
-    const int kbeg = static_cast<int>(static_cast<int64_t>(rank) * steps / S) * BK;
-    const int kend = min(g.K, static_cast<int>(static_cast<int64_t>(rank + 1) * steps / S) * BK);
-    const TI* A = static_cast<const TI*>(g.A);
-    const TI* B = static_cast<const TI*>(g.B);
-    // consecutive threads along the operand's unit stride
-    const bool a_k = g.sak == 1, b_k = g.sbk == 1;
-    float ra[TM], rb[TM];
-    auto fetch = [&](int k0) {
+    const int kbeg = SPLIT ? static_cast<int>(static_cast<int64_t>(rank) * steps / S) * BK : 0;
+    const int kend = SPLIT ? min(g.K, static_cast<int>(static_cast<int64_t>(rank + 1) * steps / S) * BK) : g.K;
+    const auto A = tiled_operand<TI, BT>(g.A, g.sam, g.sak, m0, g.M);
+    const auto B = tiled_operand<TI, BT>(g.B, g.sbn, g.sbk, n0, g.N);
+    uint64_t acc[4][TN];  // pairs of rows (2i, 2i + 1) of the thread's eight
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int e = t + 256 * i;
-            const int am = a_k ? e / BK : e % BT, ak = a_k ? e % BK : e / BT;
-            const int bn = b_k ? e / BK : e % BT, bk = b_k ? e % BK : e / BT;
-            ra[i] = (m0 + am < g.M && k0 + ak < kend) ? ld_f32<TI>(A + (m0 + am) * g.sam + (k0 + ak) * g.sak) : 0.0f;
-            rb[i] = (n0 + bn < g.N && k0 + bk < kend) ? ld_f32<TI>(B + (k0 + bk) * g.sbk + (n0 + bn) * g.sbn) : 0.0f;
-        }
-    };
-    auto stash = [&](int buf) {
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int e = t + 256 * i;
-            const int am = a_k ? e / BK : e % BT, ak = a_k ? e % BK : e / BT;
-            const int bn = b_k ? e / BK : e % BT, bk = b_k ? e % BK : e / BT;
-            sA[buf][ak][am] = ra[i];
-            sB[buf][bk][bn] = rb[i];
-        }
-    };
-    float acc[TM][TM];
-#pragma unroll
-    for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TM; ++j) acc[i][j] = 0.0f;
-    fetch(kbeg);
-    stash(0);
-    __syncthreads();
-    int buf = 0;
-    for (int k0 = kbeg; k0 < kend; k0 += BK) {
-        if (k0 + BK < kend) fetch(k0 + BK);
-        // terms beyond the range are fmaf(0, 0, acc), which leaves acc as it is
+        for (int j = 0; j < TN; ++j) acc[i][j] = 0ull;
+    // terms beyond the range are fma(0, 0, acc), which leaves acc as it is
+    auto multiply = [&](int s) {
 #pragma unroll
         for (int k = 0; k < BK; ++k) {
-            float a[TM], b[TM];
+            const float4 a0 = *reinterpret_cast<const float4*>(&sA[s][k][4 * ty]);
+            const float4 a1 = *reinterpret_cast<const float4*>(&sA[s][k][BT / 2 + 4 * ty]);
+            const uint64_t a[4] = {f2_pack(a0.x, a0.y), f2_pack(a0.z, a0.w), f2_pack(a1.x, a1.y), f2_pack(a1.z, a1.w)};
+            float b[TN];
 #pragma unroll
-            for (int i = 0; i < TM; i += 4) {
-                *reinterpret_cast<float4*>(a + i) = *reinterpret_cast<const float4*>(&sA[buf][k][16 * i + 4 * ty]);
-                *reinterpret_cast<float4*>(b + i) = *reinterpret_cast<const float4*>(&sB[buf][k][16 * i + 4 * tx]);
+            for (int j = 0; j < TN; j += 4)
+                *reinterpret_cast<float4*>(b + j) = *reinterpret_cast<const float4*>(&sB[s][k][16 * j + 4 * tx]);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const uint64_t bb = f2_splat(b[j]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[i][j] = f2_fma(a[i], bb, acc[i][j]);
             }
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-#pragma unroll
-                for (int j = 0; j < TM; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
         }
-        if (k0 + BK < kend) {
-            stash(buf ^ 1);
-            __syncthreads();
-            buf ^= 1;
+    };
+    const int n_steps = kend > kbeg ? (kend - kbeg + BK - 1) / BK : 0;
+    if constexpr (sizeof(TI) == 4) {
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s) {
+            if (s < n_steps) {
+                A.copy(sA[s], kbeg + s * BK, kend, t);
+                B.copy(sB[s], kbeg + s * BK, kend, t);
+            }
+            cp_async_commit();
+        }
+        for (int q = 0; q < n_steps; ++q) {
+            cp_async_wait<STAGES - 2>();  // tile q has arrived (this thread's part)
+            __syncthreads();              // everyone's; and tile q - 1 is no longer read
+            const int f = q + STAGES - 1;
+            if (f < n_steps) {
+                A.copy(sA[f % STAGES], kbeg + f * BK, kend, t);
+                B.copy(sB[f % STAGES], kbeg + f * BK, kend, t);
+            }
+            cp_async_commit();
+            multiply(q % STAGES);
+        }
+        cp_async_wait<0>();
+    } else {
+        TI ra[TiledOperand<TI, BT>::PER], rb[TiledOperand<TI, BT>::PER];
+        if (n_steps > 0) {
+            A.fetch(ra, kbeg, kend, t);
+            B.fetch(rb, kbeg, kend, t);
+        }
+        for (int q = 0; q < n_steps; ++q) {
+            A.stash(sA[q & 1], ra, t);
+            B.stash(sB[q & 1], rb, t);
+            __syncthreads();  // tile q is there; tile q - 1 (the other buffer) may still be read
+            if (q + 1 < n_steps) {
+                A.fetch(ra, kbeg + (q + 1) * BK, kend, t);
+                B.fetch(rb, kbeg + (q + 1) * BK, kend, t);
+            }
+            multiply(q & 1);
         }
     }
-    if constexpr (BT == 64) {
-        if (S > 1) {
-            const int own = 64 / S;  // rows per block; S divides 64
+    if constexpr (SPLIT) {
+        static_assert(TN == 4, "64-wide tiles");
+        // the sums of rank q's part: [q][row of this block's][column], in the
+        // ring's memory once every block of the cluster is through with its own
+        float* parts = &sA[0][0][0];
+        static_assert(sizeof(sA) >= 64 * 64 * 4 || sizeof(TI) != 4, "parts fit the A ring");
+        __shared__ __align__(16) float own_parts[sizeof(TI) == 4 ? 1 : 64 * 64];
+        if constexpr (sizeof(TI) != 4) parts = own_parts;
+        else cluster_sync();
+        const int own = 64 / S;  // rows per block; S divides 64
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = 4 * ty + i;
-                const uint32_t dst = mapa_shared(smem_u32(parts + (rank * own + row % own) * 64 + 4 * tx), row / own);
+        for (int i = 0; i < 4; ++i) {
+            float lo[4], hi[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) st_shared_cluster_u32(dst + 4 * j, __float_as_uint(acc[i][j]));
+            for (int j = 0; j < 4; ++j) f2_unpack(acc[i][j], lo[j], hi[j]);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int row = (i & 2) * 16 + 4 * ty + 2 * (i & 1) + r;
+                const float* v = r == 0 ? lo : hi;
+                st_shared_cluster_v4(mapa_shared(smem_u32(parts + (rank * own + row % own) * 64 + 4 * tx), row / own),
+                                     v[0], v[1], v[2], v[3]);
             }
-            cluster_sync();  // every block's sums of this block's rows have arrived
-            for (int e = t; e < own * 64; e += 256) {
-                const int row = e / 64, col = e % 64;
-                float v = parts[row * 64 + col];
-                for (int q = 1; q < S; ++q) v += parts[(q * own + row) * 64 + col];
-                const int64_t m = m0 + rank * own + row, n = n0 + col;
-                if (m < g.M && n < g.N) tiled_store<TI, TO, EPI>(p, m, n, v);
-            }
-            return;
         }
-    }
+        cluster_sync();  // every block's sums of this block's rows have arrived
+        for (int e = t; e < own * 64; e += NT) {
+            const int row = e / 64, col = e % 64;
+            float v = parts[row * 64 + col];
+            for (int q = 1; q < S; ++q) v += parts[(q * own + row) * 64 + col];
+            const int64_t m = m0 + rank * own + row, n = n0 + col;
+            if (m < g.M && n < g.N) tiled_store<TI, TO, EPI>(p, m, n, v);
+        }
+    } else {
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int64_t m = m0 + 16 * (i & ~3) + 4 * ty + (i & 3);
-        if constexpr (EpiTraits<EPI>::kC8Out) {
-            // 32 columns of a row are 8 neighbouring threads' groups of four
+        for (int i = 0; i < 8; ++i) {
+            const int64_t m = m0 + (i & 4) * (BT / 8) + 4 * ty + (i & 3);
+            float v[TN];
 #pragma unroll
-            for (int j = 0; j < TM; j += 4) {
-                const int64_t n = n0 + 16 * j + 4 * tx;
-                float top = 0.0f;
+            for (int j = 0; j < TN; ++j) {
+                float lo, hi;
+                f2_unpack(acc[i / 2][j], lo, hi);
+                v[j] = (i & 1) ? hi : lo;
+            }
+#pragma unroll
+            for (int j = 0; j < TN; j += 4) {
+                const int64_t n = n0 + column(j);
+                if constexpr (EpiTraits<EPI>::kC8Out) {
+                    // 32 columns of a row are 8 neighbouring threads' groups of four
+                    float* x = v + j;
+                    float top = 0.0f;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        if (g.bias != nullptr && n + c < g.N) x[c] += ld_f32<TI>(static_cast<const TI*>(g.bias) + n + c);
+                        top = max_nan(top, fabsf(x[c]));
+                    }
+                    for (int w = 1; w < 8; w <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, w));
+                    const uint32_t sb = c8_scale_byte(top);
+                    const uint32_t word = sb == kC8NaN ? 0u : c8_pack4(x[0], x[1], x[2], x[3], c8_inverse(sb));
+                    if (m < g.M && n < p.c8_ld) *reinterpret_cast<uint32_t*>(p.c8 + m * p.c8_ld + n) = word;
+                    if (m < g.M && n < g.N && (tx & 7) == 0)
+                        p.c8_scale[n / kC8Block * g.M + m] = static_cast<uint8_t>(sb);
+                }
+                if (m >= g.M) continue;
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    if (g.bias != nullptr && n + c < g.N)
-                        acc[i][j + c] += ld_f32<TI>(static_cast<const TI*>(g.bias) + n + c);
-                    top = max_nan(top, fabsf(acc[i][j + c]));
+                    const int64_t nc = n0 + column(j + c);
+                    if (nc < g.N) tiled_store<TI, TO, EPI>(p, m, nc, v[j + c]);
                 }
-                for (int w = 1; w < 8; w <<= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, w));
-                const uint32_t sb = c8_scale_byte(top);
-                const uint32_t word = sb == kC8NaN ? 0u : c8_pack4(acc[i][j], acc[i][j + 1], acc[i][j + 2],
-                                                                   acc[i][j + 3], c8_inverse(sb));
-                if (m < g.M && n < p.c8_ld) *reinterpret_cast<uint32_t*>(p.c8 + m * p.c8_ld + n) = word;
-                if (m < g.M && n < g.N && (tx & 7) == 0)
-                    p.c8_scale[n / kC8Block * g.M + m] = static_cast<uint8_t>(sb);
             }
-        }
-        if (m >= g.M) continue;
-#pragma unroll
-        for (int j = 0; j < TM; ++j) {
-            const int64_t n = n0 + 16 * (j & ~3) + 4 * tx + (j & 3);
-            if (n < g.N) tiled_store<TI, TO, EPI>(p, m, n, acc[i][j]);
         }
     }
 }

@@ -24,9 +24,12 @@ bool fits32(int64_t x) { return x < (int64_t(1) << 31); }
 // ------------------------------------------------------------- plain products
 
 // One product, or two of the same kind in one launch (q may be null). Tiles
-// of 128 × 128 (8 × 8 outputs a thread) where they still are two per SM, else
-// 64 × 64; with fewer of those than SMs, K is split over a cluster of up to 8
-// blocks (at least four 16-deep steps each).
+// of 128 × 128 where there are enough for the SMs (fp32: three for four SMs,
+// 2048 × 1024, K = 1024 127 µs against 131-158 with 64 × 64; bf16, whose operands
+// are converted on the way: two per SM, 166 against 146), else 64 × 64, four
+// blocks to an SM; with fewer tiles than that, K is split over a cluster of up to
+// 8 blocks (at least eight 16-deep steps before each doubling: 512³ fp32 35 / 22 /
+// 16.5 / 16.4 µs with 1 / 2 / 4 / 8).
 template <typename TI, typename TO, int EPI>
 tpmlp_status gemm_plain(int kind, TiledProduct p, cudaStream_t st, const TiledProduct* q = nullptr) {
     double flops = 0.0, bytes = 0.0;
@@ -40,10 +43,10 @@ tpmlp_status gemm_plain(int kind, TiledProduct p, cudaStream_t st, const TiledPr
         tiles64 += ((int64_t(x->a.M) + 63) / 64) * ((int64_t(x->a.N) + 63) / 64);
     }
     const int sms = plan_num_sms();
-    const int bt = tiles128 >= 2 * sms ? 128 : 64;
+    const int bt = (sizeof(TI) == 4 ? 4 * tiles128 >= 3 * sms : tiles128 >= 2 * sms) ? 128 : 64;
     int S = 1;
     if (bt == 64 && !EpiTraits<EPI>::kC8Out)
-        while (S < 8 && tiles64 * S * 2 <= 2 * sms && k >= 128 * S) S *= 2;
+        while (S < 8 && tiles64 * S * 2 <= 4 * sms && k >= 128 * S) S *= 2;
     TiledProduct none{};
     TiledProduct p1 = q != nullptr ? *q : none;
     for (TiledProduct* x : {&p, &p1}) {
@@ -53,7 +56,7 @@ tpmlp_status gemm_plain(int kind, TiledProduct p, cudaStream_t st, const TiledPr
     return timed(kind, flops, bytes, st, [&] {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(static_cast<unsigned>(bt == 128 ? tiles128 : tiles64), 1, static_cast<unsigned>(S));
-        cfg.blockDim = dim3(256);
+        cfg.blockDim = dim3(bt == 128 ? 256 : 128);
         cfg.stream = st;
         cudaLaunchAttribute attr;
         attr.id = cudaLaunchAttributeClusterDimension;
@@ -62,8 +65,14 @@ tpmlp_status gemm_plain(int kind, TiledProduct p, cudaStream_t st, const TiledPr
         attr.val.clusterDim.z = static_cast<unsigned>(S);
         cfg.attrs = &attr;
         cfg.numAttrs = S > 1 ? 1 : 0;
-        const cudaError_t e = bt == 128 ? cudaLaunchKernelEx(&cfg, simt_tiled_kernel<TI, TO, EPI, 128>, p, p1, S)
-                                        : cudaLaunchKernelEx(&cfg, simt_tiled_kernel<TI, TO, EPI, 64>, p, p1, S);
+        cudaError_t e;
+        if (bt == 128) {
+            e = cudaLaunchKernelEx(&cfg, simt_tiled_kernel<TI, TO, EPI, 128, false>, p, p1, S);
+        } else if (S == 1) {
+            e = cudaLaunchKernelEx(&cfg, simt_tiled_kernel<TI, TO, EPI, 64, false>, p, p1, S);
+        } else if constexpr (!EpiTraits<EPI>::kC8Out) {
+            e = cudaLaunchKernelEx(&cfg, simt_tiled_kernel<TI, TO, EPI, 64, true>, p, p1, S);
+        }
         g_launches.fetch_add(1, std::memory_order_relaxed);
         if (e != cudaSuccess) cudaGetLastError();
         return e == cudaSuccess ? TPMLP_OK : TPMLP_ERR_CUDA;
