@@ -217,8 +217,8 @@ __global__ void __launch_bounds__(256) ckpt8_decode_kernel(const uint8_t* __rest
 // The CUDA-core product of simt.cuh with register tiles: BT × BT outputs per
 // block (64 or 128), 8 × BT/16 a thread as packed pairs of fp32 (two rows), and
 // 16-deep k tiles in shared memory. fp32 operands come through a ring of
-// asynchronous copies, 16 bytes where rows allow it; bf16 operands are converted
-// on the way, one tile ahead in registers. Each output is an fp32 accumulator
+// asynchronous copies, 16 bytes where rows allow it, or, 16 bytes along k, through
+// registers; bf16 operands are converted on the way, one tile ahead in registers. Each output is an fp32 accumulator
 // updated with fma over k in ascending order. SPLIT (BT = 64): a cluster of S
 // blocks takes consecutive parts of K, and each block adds the parts of its 64/S
 // rows in ascending k (few output tiles and a long K: weight gradients of narrow
@@ -274,7 +274,35 @@ struct TiledOperand {
     const TI* p;  // at the tile's first row
     int64_t sx, sk;
     int left;  // rows of the tile inside the matrix
-    bool k_unit, vec;
+    bool k_unit, vec, kvec;
+
+    // fp32, k the unit stride, 16-byte loads of 4 elements aligned: through
+    // registers, transposed on the way into s
+    __device__ __forceinline__ void fetch4(float4 (&r)[PER / 4], int k0, int kend, int t) const {
+#pragma unroll
+        for (int i = 0; i < PER / 4; ++i) {
+            const int e = t + NT * i, x = e / (BK / 4), k = k0 + e % (BK / 4) * 4;
+            r[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const float* q = reinterpret_cast<const float*>(p) + x * sx + k;
+            if (x < left && k + 3 < kend) {
+                r[i] = *reinterpret_cast<const float4*>(q);
+            } else if (x < left) {
+                if (k < kend) r[i].x = q[0];
+                if (k + 1 < kend) r[i].y = q[1];
+                if (k + 2 < kend) r[i].z = q[2];
+            }
+        }
+    }
+    __device__ __forceinline__ void stash4(float (*s)[LD], const float4 (&r)[PER / 4], int t) const {
+#pragma unroll
+        for (int i = 0; i < PER / 4; ++i) {
+            const int e = t + NT * i, x = e / (BK / 4), k = e % (BK / 4) * 4;
+            s[k][x] = r[i].x;
+            s[k + 1][x] = r[i].y;
+            s[k + 2][x] = r[i].z;
+            s[k + 3][x] = r[i].w;
+        }
+    }
 
     // element e of the tile: consecutive threads along the unit stride
     __device__ __forceinline__ void place(int e, int& x, int& k) const {
@@ -327,7 +355,9 @@ __device__ __forceinline__ TiledOperand<TI, BT> tiled_operand(const void* base, 
     o.sk = sk;
     o.left = static_cast<int>(min(static_cast<int64_t>(BT), extent - x0));
     o.k_unit = sk == 1;
-    o.vec = sx == 1 && sk % 4 == 0 && (reinterpret_cast<uintptr_t>(base) & 15u) == 0;
+    const bool aligned = sizeof(TI) == 4 && (reinterpret_cast<uintptr_t>(base) & 15u) == 0;
+    o.vec = sx == 1 && sk % 4 == 0 && aligned;
+    o.kvec = sk == 1 && sx % 4 == 0 && sx > 1 && aligned;  // (a k tile starts at a multiple of 16)
     return o;
 }
 
@@ -381,11 +411,16 @@ __global__ void __launch_bounds__(BT == 128 ? 256 : 128, BT == 128 ? 2 : 4)
     };
     const int n_steps = kend > kbeg ? (kend - kbeg + BK - 1) / BK : 0;
     if constexpr (sizeof(TI) == 4) {
+        float4 ra[TiledOperand<TI, BT>::PER / 4], rb[TiledOperand<TI, BT>::PER / 4];
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s) {
             if (s < n_steps) {
-                A.copy(sA[s], kbeg + s * BK, kend, t);
-                B.copy(sB[s], kbeg + s * BK, kend, t);
+                if (A.kvec) A.fetch4(ra, kbeg + s * BK, kend, t);
+                else A.copy(sA[s], kbeg + s * BK, kend, t);
+                if (B.kvec) B.fetch4(rb, kbeg + s * BK, kend, t);
+                else B.copy(sB[s], kbeg + s * BK, kend, t);
+                if (A.kvec) A.stash4(sA[s], ra, t);
+                if (B.kvec) B.stash4(sB[s], rb, t);
             }
             cp_async_commit();
         }
@@ -394,11 +429,18 @@ __global__ void __launch_bounds__(BT == 128 ? 256 : 128, BT == 128 ? 2 : 4)
             __syncthreads();              // everyone's; and tile q - 1 is no longer read
             const int f = q + STAGES - 1;
             if (f < n_steps) {
-                A.copy(sA[f % STAGES], kbeg + f * BK, kend, t);
-                B.copy(sB[f % STAGES], kbeg + f * BK, kend, t);
+                if (A.kvec) A.fetch4(ra, kbeg + f * BK, kend, t);
+                else A.copy(sA[f % STAGES], kbeg + f * BK, kend, t);
+                if (B.kvec) B.fetch4(rb, kbeg + f * BK, kend, t);
+                else B.copy(sB[f % STAGES], kbeg + f * BK, kend, t);
             }
             cp_async_commit();
             multiply(q % STAGES);
+            // the stage is free: tile q - 1 was its last, before this round's barrier
+            if (f < n_steps) {
+                if (A.kvec) A.stash4(sA[f % STAGES], ra, t);
+                if (B.kvec) B.stash4(sB[f % STAGES], rb, t);
+            }
         }
         cp_async_wait<0>();
     } else {

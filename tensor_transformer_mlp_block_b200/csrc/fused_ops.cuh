@@ -24,12 +24,12 @@ bool fits32(int64_t x) { return x < (int64_t(1) << 31); }
 // ------------------------------------------------------------- plain products
 
 // One product, or two of the same kind in one launch (q may be null). Tiles
-// of 128 × 128 where there are enough for the SMs (fp32: three for four SMs,
-// 2048 × 1024, K = 1024 127 µs against 131-158 with 64 × 64; bf16, whose operands
-// are converted on the way: two per SM, 166 against 146), else 64 × 64, four
-// blocks to an SM; with fewer tiles than that, K is split over a cluster of up to
-// 8 blocks (at least eight 16-deep steps before each doubling: 512³ fp32 35 / 22 /
-// 16.5 / 16.4 µs with 1 / 2 / 4 / 8).
+// of 128 × 128 where there are four per SM, else 64 × 64, of which an SM holds
+// four; with fewer than eight per SM, K is split over a cluster of up to 8 blocks
+// (at least four 16-deep steps each). Measured on B200, fp32, µs with 64 × 64
+// unsplit and split 2 / 4 / 8 ways: 2048 × 1024, K = 1024 123 and 109 / 119 / 127
+// (123 with 128 × 128); 1024 × 1024, K = 2048 135 and 124 / 122 / 119 (238); 512³
+// 29 and 18.5 / 14.5 / 14.4 (64).
 template <typename TI, typename TO, int EPI>
 tpmlp_status gemm_plain(int kind, TiledProduct p, cudaStream_t st, const TiledProduct* q = nullptr) {
     double flops = 0.0, bytes = 0.0;
@@ -43,10 +43,10 @@ tpmlp_status gemm_plain(int kind, TiledProduct p, cudaStream_t st, const TiledPr
         tiles64 += ((int64_t(x->a.M) + 63) / 64) * ((int64_t(x->a.N) + 63) / 64);
     }
     const int sms = plan_num_sms();
-    const int bt = (sizeof(TI) == 4 ? 4 * tiles128 >= 3 * sms : tiles128 >= 2 * sms) ? 128 : 64;
+    const int bt = tiles128 >= 4 * sms ? 128 : 64;
     int S = 1;
     if (bt == 64 && !EpiTraits<EPI>::kC8Out)
-        while (S < 8 && tiles64 * S * 2 <= 4 * sms && k >= 128 * S) S *= 2;
+        while (S < 8 && tiles64 * S * 2 <= 8 * sms && k >= 128 * S) S *= 2;
     TiledProduct none{};
     TiledProduct p1 = q != nullptr ? *q : none;
     for (TiledProduct* x : {&p, &p1}) {
