@@ -23,6 +23,8 @@
  *    returns an error has enqueued nothing.
  *  - Results are deterministic: the same inputs and p give bit-identical
  *    outputs on every run.
+ *  - A workspace serves one call at a time: calls, or captured graphs, whose
+ *    kernels may run at once need one each. Its contents need not be kept.
  *  - The library keeps a small amount of process-wide state (the split
  *    policy, the wait limit, a launch counter, per-device caches, one device
  *    status word per device). Its caches are guarded, so host threads may

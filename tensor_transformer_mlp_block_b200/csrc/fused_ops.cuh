@@ -19,7 +19,8 @@ tpmlp_status check_device() {
 bool known_dtype(tpmlp_dtype dt) { return dt == TPMLP_BF16 || dt == TPMLP_FP32; }
 bool known_act(tpmlp_activation a) { return a == TPMLP_GELU_ERF || a == TPMLP_GELU_TANH; }
 bool known_grad(tpmlp_dtype g, tpmlp_dtype dt) { return g == TPMLP_FP32 || (g == TPMLP_BF16 && dt == TPMLP_BF16); }
-bool fits32(int64_t x) { return x < (int64_t(1) << 31); }
+// Sizes that the kernels' 32-bit row and column indices hold, tiles' last rows included.
+bool fits32(int64_t x) { return x < (int64_t(1) << 31) - 1024; }
 
 // ------------------------------------------------------------- plain products
 
@@ -434,6 +435,7 @@ tpmlp_status linear_fwd_ex_impl(const void* X, const void* W, const void* bias, 
     if (act == TPMLP_ACT_NONE && H != nullptr) return TPMLP_ERR_INVALID;
     if (T == 0) return TPMLP_OK;
     if (!X || !W || !Y) return TPMLP_ERR_INVALID;
+    if (!fits32(T) || !fits32(K) || !fits32(N)) return TPMLP_ERR_UNSUPPORTED;
     // the relaying activation epilogues run whole tiles (kSplittable)
     const SchedReq req = (act != TPMLP_ACT_NONE && K >= kRelayMinKAct) ? SchedReq{} : pl.fwd;
     const bool splits = pl.tc && T > kFewMaxRows && req.kind != SCHED_TILES;
@@ -565,6 +567,7 @@ tpmlp_status c8_checks(int64_t T, int64_t h, int64_t F, int p, tpmlp_dtype dt, t
                        void* ws, size_t ws_bytes, bool need_ws) {
     if (!known_act(act)) return TPMLP_ERR_INVALID;
     TPMLP_TRY(common_checks(T, h, F, p, dt, pl, ws, ws_bytes, need_ws));
+    if (!fits32(T) || !fits32(h) || !fits32(F)) return TPMLP_ERR_UNSUPPORTED;
     if (!plain_grid_ok(T, F) || !plain_grid_ok(T, h) || !plain_grid_ok(h, F) || pl->chunks > kMaxGridY)
         return TPMLP_ERR_UNSUPPORTED;
     return TPMLP_OK;
@@ -809,7 +812,7 @@ tpmlp_status tp_linear_bwd_ex(const void* dY, const void* X, const void* W, cons
                               static_cast<const void*>(dbias), static_cast<const void*>(dH)})
             if (q && !aligned16(q)) return TPMLP_ERR_ALIGN;
     }
-    if (!columns_ok(N) || !plain_grid_ok(K, N) || !plain_grid_ok(T, K) || pl.chunks > kMaxGridY)
+    if (!fits32(T) || !fits32(K) || !fits32(N) || !columns_ok(N) || !plain_grid_ok(K, N) || !plain_grid_ok(T, K) || pl.chunks > kMaxGridY)
         return TPMLP_ERR_UNSUPPORTED;
     if (dt == TPMLP_FP32)
         return linear_bwd_ex_run<float, float>(pl, dY, X, W, H, dX, dW, dbias, dH, T, K, N, act, workspace, st);

@@ -175,6 +175,39 @@ def test_long_products(act):
     assert binding.last_device_status() == binding.OK
 
 
+@pytest.mark.parametrize("T,h,F", [(8192, 12288, 9472), (8192, 4096, 32768)])
+def test_dynamic_schedule_gives_the_same(T, h, F):
+    """Products long enough for the dynamic schedule (the first and third, then the second and last): bit for bit
+    what the static one gives; rows of the results against the formulas."""
+    v = make(T, h, F, "bf16", seed=2)
+    assert any(binding.plan_dynamic(T, h, F, 1).values())
+    got = []
+    for on in (True, False):
+        binding.set_dynamic_schedule(on)
+        try:
+            C, S, Z = binding.forward_ckpt8(v["X"], v["A"], v["a"], v["B"], v["b"], 1, residual=v["R"])
+            g = binding.backward_ckpt8(v["dZ"], v["X"], v["A"], v["B"], C, S, 1, grad_dtype=torch.bfloat16)
+            got.append(dict(C=C, S=S, Z=Z, **{k: g[k] for k in ("dX", "dH", "Y", "dA", "da", "dB", "db")}))
+        finally:
+            binding.set_dynamic_schedule(True)
+    for k in got[0]:
+        assert torch.equal(got[0][k], got[1][k]), k
+    assert binding.last_device_status() == binding.OK
+    rows = torch.tensor([0, 77, T - 1], device="cuda")
+    part = {k: (t[rows] if k in ("X", "R", "dZ") else t) for k, t in v.items()}
+    x, A, B, z = (part[k].double() for k in ("X", "A", "B", "dZ"))
+    hh = x @ A + part["a"].double()
+    C, S = got[0]["C"][rows], got[0]["S"][:, rows].contiguous()
+    step = torch.ldexp(torch.ones_like(hh), (S.t().int() - 127).repeat_interleave(32, 1)[:, :F])
+    bound = step / 2 + product_error(x, A) + 2 * U * hh.abs()
+    assert ((eight_bit_values(C, S, F) - hh).abs() <= bound).all()
+    y, d = act64(eight_bit_values(C, S, F), "gelu")
+    p = z @ B.t()
+    close(got[0]["dH"][rows], p * d, SLOPE * product_error(z, B.t()) + p.abs() * ACT * 6 + U * (p * d).abs(), "dH")
+    dH = got[0]["dH"][rows].double()
+    close(got[0]["dX"][rows], dH @ A.t(), product_error(dH, A.t()), "dX")
+
+
 def test_agrees_with_the_block_that_keeps_h():
     """The forward's product and residual are forward()'s; the gradients differ by the checkpoint's rounding: at
     most 1/127 of a block's largest magnitude, a relative error of the gradients of a few parts in a thousand."""

@@ -160,6 +160,41 @@ def test_long_and_relayed_products(T, K):
     assert binding.last_device_status() == binding.OK
 
 
+def test_long_product_variant():
+    """Four waves of tiles and 64 k-blocks: the kernels with two staging slots per warp."""
+    v = make(8200, 4096, 2568, "bf16", seed=1)
+    for act in ("none", "gelu", "gelu_tanh"):
+        check_forward(v, act, binding.fused_linear_forward(v["X"], v["W"], v["bias"], activation=act,
+                                                           residual=v["R"]))
+        if act != "none":
+            Y, H = binding.fused_linear_forward(v["X"], v["W"], v["bias"], activation=act, residual=v["R"],
+                                                keep_hidden=True)
+            check_forward(v, act, Y, H)
+    R = v["R"].clone()
+    binding.fused_linear_forward(v["X"], v["W"], v["bias"], residual=R, out=R)
+    check_forward(v, "none", R)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_offsets_past_32_bits(dtype):
+    """More than 2^31 outputs: the last rows come out right."""
+    T, K, N = 70016, 16, 33000
+    v = make(300, K, N, dtype, seed=2)
+    X = torch.zeros(T, K, dtype=DT[dtype], device="cuda")
+    X[-300:] = v["X"]
+    Y = binding.fused_linear_forward(X, v["W"], v["bias"], activation="gelu")
+    want = binding.fused_linear_forward(v["X"], v["W"], v["bias"], activation="gelu")
+    zero = binding.fused_linear_forward(X[:300].contiguous(), v["W"], v["bias"], activation="gelu")
+    # (another number of rows may mean another kernel and order of sums: 16 products)
+    assert float((Y[-300:].double() - want.double()).abs().max()) <= 2 ** -7 * float(want.double().abs().max())
+    assert torch.equal(Y[:300], zero) and torch.equal(Y[35000], zero[0])
+    del want, zero
+    if dtype == "bf16":
+        dX, dW, db = binding.fused_linear_backward(Y, X, v["W"])
+        ref = Y[-300:].double() @ v["W"].double().t()
+        close(dX[-300:], ref, product_error(Y[-300:].double(), v["W"].double().t()), "dX")
+
+
 @pytest.mark.parametrize("T", [1, 16, 64, 200])
 def test_residual_in_place(T):
     v = make(T, 512, 768, "bf16", seed=T)
