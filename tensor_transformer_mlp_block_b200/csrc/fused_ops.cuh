@@ -352,7 +352,7 @@ tpmlp_status gemm_few_launch(const void* X, const void* W, int T, int N, int K, 
     auto kern = gemm_few_kernel<TN>;
     {
         std::lock_guard<std::mutex> lock(g_dev_mutex);
-        static bool set[kMaxDevices] = {};
+        static bool set[kMaxDevices] = {};  // guarded by the lock
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return TPMLP_ERR_CUDA;
         if (!set[dev]) {
@@ -362,10 +362,10 @@ tpmlp_status gemm_few_launch(const void* X, const void* W, int T, int N, int K, 
             set[dev] = true;
         }
     }
-    const int tn = (N + kFewCols - 1) / kFewCols, tt = (T + TN - 1) / TN;
-    const int S = few_split(int64_t(tn) * tt, g.k_blocks, Cfg::CTAS);
+    const int tiles = (N + kFewCols - 1) / kFewCols;
+    const int S = few_split(tiles, g.k_blocks, Cfg::CTAS);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(tn * S), static_cast<unsigned>(tt));
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * S));
     cfg.blockDim = dim3(kFewThreads);
     cfg.dynamicSmemBytes = Cfg::SMEM_BYTES;
     cfg.stream = st;
@@ -392,8 +392,8 @@ constexpr int64_t kFewMaxRows = 128;
 
 static_assert(kFewMaxRows >= kBM, "gemm_tc_pick relies on it");
 
-tpmlp_status linear_few(int kind, const void* X, const void* W, const void* bias, const void* R, void* H, void* Y, int T, int N,
-                        int K, tpmlp_activation act, cudaStream_t st) {
+tpmlp_status linear_few(int kind, const void* X, const void* W, const void* bias, const void* R, void* H, void* Y,
+                        int T, int N, int K, tpmlp_activation act, cudaStream_t st) {
     FewArgs g{};
     g.act = static_cast<int>(act);
     g.bias = static_cast<const bf16*>(bias);
@@ -476,7 +476,7 @@ tpmlp_status linear_fwd_ex_impl(const void* X, const void* W, const void* bias, 
 
 // Rows per block of act_grad_kernel: all 32 in flight at once, and blocks small
 // enough that a last, partly filled wave of them costs little (with 128 rows,
-// 6144 × 4096 is 1.04 waves of 740 blocks: 44 µs, against 30).
+// 6144 × 4096 is 1.04 waves of 740 blocks: 44 µs, against 32).
 constexpr int64_t kActGradRows = 32;
 
 int64_t act_grad_chunks(int64_t T) { return T > 0 ? (T + kActGradRows - 1) / kActGradRows : 1; }
@@ -558,7 +558,8 @@ tpmlp_status ckpt8_encode_launch(const void* H, void* C, void* S, int64_t R, int
 template <typename T>
 tpmlp_status ckpt8_decode_launch(const void* C, const void* S, void* H, int64_t R, int64_t F, cudaStream_t st) {
     const dim3 grid(static_cast<unsigned>((R + 31) / 32), static_cast<unsigned>((F + 255) / 256));
-    auto kern = F % 8 == 0 && aligned16(H) ? ckpt8_decode_kernel<T, true> : ckpt8_decode_kernel<T, false>;
+    constexpr int W = 16 / static_cast<int>(sizeof(T));
+    auto kern = F % W == 0 && aligned16(H) ? ckpt8_decode_kernel<T, W> : ckpt8_decode_kernel<T, 1>;
     return launch_dep(kern, grid, dim3(256), 0, st, static_cast<const uint8_t*>(C),
                       static_cast<const uint8_t*>(S), static_cast<T*>(H), R, F);
 }
@@ -812,7 +813,8 @@ tpmlp_status tp_linear_bwd_ex(const void* dY, const void* X, const void* W, cons
                               static_cast<const void*>(dbias), static_cast<const void*>(dH)})
             if (q && !aligned16(q)) return TPMLP_ERR_ALIGN;
     }
-    if (!fits32(T) || !fits32(K) || !fits32(N) || !columns_ok(N) || !plain_grid_ok(K, N) || !plain_grid_ok(T, K) || pl.chunks > kMaxGridY)
+    if (!fits32(T) || !fits32(K) || !fits32(N) || !columns_ok(N) || !plain_grid_ok(K, N) ||
+        !plain_grid_ok(T, K) || pl.chunks > kMaxGridY)
         return TPMLP_ERR_UNSUPPORTED;
     if (dt == TPMLP_FP32)
         return linear_bwd_ex_run<float, float>(pl, dY, X, W, H, dX, dW, dbias, dH, T, K, N, act, workspace, st);

@@ -1,16 +1,22 @@
 // Product of few rows with a weight matrix, with bias, activation and
-// residual: Y[T, N] = act(X·W + bias) + R for up to a few hundred rows (single
-// tokens, small batches, short prompts).
+// residual: Y[T, N] = act(X·W + bias) + R for up to 128 rows (single tokens,
+// small batches, short prompts).
 //
 // With few rows the time is that of reading W once from memory, so the work is
 // cut to keep every SM loading: the output's transpose is computed, 128 columns
 // of W per tile as the tensor cores' 128 rows (W [K][N] is read MN-major, as it
-// lies) and TN rows of X as their N, and the tile's K range is split over a
+// lies) and TN ≥ T rows of X as their N, and the tile's K range is split over a
 // cluster of S CTAs. Each CTA streams its part of W through a shared-memory
-// ring. Every CTA of the cluster owns ⌈128/S⌉ of the tile's columns: the others store their fp32 partial sums of them straight into its
-// shared memory, and after one cluster barrier it adds them in ascending k. So
-// nothing goes through global memory, no counters are needed, and the result
-// does not depend on timing.
+// ring. Every CTA of the cluster owns 128/S of the tile's columns: the others
+// store their fp32 partial sums of them straight into its shared memory, and
+// after one cluster barrier it adds them in ascending k. So nothing goes through
+// global memory, no counters are needed, and the result does not depend on
+// timing. (Sums read from the other CTAs after the barrier took 5 µs more.)
+//
+// Measured on B200: 1 row, 4096 → 16384, GeLU 24.3 µs and 24 rows, 16384 → 4096
+// with a residual 26.4 µs, for 134 MB of W, 20.5 µs at the measured copy rate;
+// one 128-row tile per CTA without the split took 51 and 61 µs. What is left is
+// the start (barriers, tensor memory, the first loads) and the sums' exchange.
 //
 // 192 threads: warp 0 TMA producer, warp 1 MMA issuer, warps 2..5 epilogue
 // (each the 32 tensor-memory lanes, i.e. columns of W, of its sub-partition).
@@ -29,8 +35,8 @@ struct FewCfg {
     static constexpr int W_BYTES = kFewCols * kBK * 2;
     static constexpr int X_BYTES = TN * kBK * 2;
     static constexpr int STAGE_BYTES = W_BYTES + X_BYTES;
-    // partial sums of this CTA's columns: [rank][row][column], S·⌈128/S⌉ <= 135
-    static constexpr int PART_BYTES = TN * 136 * 4;
+    // partial sums of this CTA's columns: [rank][row][column], 128/S columns
+    static constexpr int PART_BYTES = TN * kFewCols * 4;
     // Two CTAs per SM (at most 113 KB each), so that one's prologue and sums
     // run beside the other's loads; a tile of 128 rows leaves room for one.
     static constexpr int CTAS = TN <= 64 ? 2 : 1;
@@ -62,7 +68,7 @@ __device__ __forceinline__ void few_store(const FewArgs& g, int t, int n, float 
     g.Y[off] = __float2bfloat16_rn(v);
 }
 
-// Grid (tiles of W's columns × S, tiles of TN rows), cluster (S, 1).
+// Grid: tiles of W's columns × S, in clusters of S (a power of two).
 template <int TN>
 __global__ void __launch_bounds__(kFewThreads, FewCfg<TN>::CTAS)
     gemm_few_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
@@ -88,7 +94,6 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<TN>::CTAS)
     const int lane = threadIdx.x & 31;
     const int rank = S > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     const int n0 = static_cast<int>(blockIdx.x) / S * kFewCols;
-    const int t0 = static_cast<int>(blockIdx.y) * TN;
     const int kb0 = static_cast<int>(static_cast<int64_t>(rank) * g.k_blocks / S);
     const int kb1 = static_cast<int>(static_cast<int64_t>(rank + 1) * g.k_blocks / S);
 
@@ -131,7 +136,7 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<TN>::CTAS)
                 const uint32_t w_dst = smem_u32(sW + s * C::W_BYTES);
                 tma_load_2d(w_dst, &tmW, fb, n0, kb * kBK);
                 tma_load_2d(w_dst + 8192, &tmW, fb, n0 + 64, kb * kBK);
-                tma_load_2d(smem_u32(sX + s * C::X_BYTES), &tmX, fb, kb * kBK, t0);
+                tma_load_2d(smem_u32(sX + s * C::X_BYTES), &tmX, fb, kb * kBK, 0);
             }
             // every slot's last release has arrived before this CTA may exit
             for (int i = issued > STAGES ? issued - STAGES : 0; i < issued && !*abort; ++i)
@@ -173,11 +178,11 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<TN>::CTAS)
     } else {
         const int quad = warp & 3;
         const int c = quad * 32 + lane;  // column of W within the tile
-        const int rows = min(TN, g.T - t0);
+        const int rows = g.T;
         if (g.resid != nullptr && (lane & 15) == 0 && n0 + c < g.N) {
             // the residual's first touch of memory runs beside the product
             for (int t = rank; t < rows; t += S)
-                prefetch_l2(g.resid + static_cast<int64_t>(t0 + t) * g.N + n0 + c);
+                prefetch_l2(g.resid + static_cast<int64_t>(t) * g.N + n0 + c);
         }
         // every lane waits and the warp goes on only together (.sync.aligned loads)
         ok = mbar_wait_bounded(smem_u32(done), 0, abort, limit);
@@ -190,7 +195,7 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<TN>::CTAS)
             float bias = 0.0f;
             if (S == 1 && g.bias != nullptr && n < g.N) bias = __bfloat162float(g.bias[n]);
             // the owner of column c, and where this rank's sums of it go
-            const int cols = (kFewCols + S - 1) / S;
+            const int cols = kFewCols / S;
             const uint32_t dst = S > 1 ? mapa_shared(smem_u32(parts + rank * TN * cols + c % cols), c / cols) : 0u;
 #pragma unroll 1
             for (int j = 0; j < rows; j += 16) {
@@ -200,7 +205,7 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<TN>::CTAS)
                 if (S == 1) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if (j + i < rows && n < g.N) few_store(g, t0 + j + i, n, __uint_as_float(v[i]), bias);
+                        if (j + i < rows && n < g.N) few_store(g, j + i, n, __uint_as_float(v[i]), bias);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
@@ -213,22 +218,19 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<TN>::CTAS)
     if (S > 1) {
         cluster_sync();  // every rank's sums of this rank's columns have arrived
         if (warp >= 2 && ok) {
-            const int cols = (kFewCols + S - 1) / S;
-            const int rows = min(TN, g.T - t0);
+            const int cols = kFewCols / S;  // S rows at a time, one column a thread
             const int e = static_cast<int>(threadIdx.x) - 64;
-            const int per = 128 / cols;  // rows at a time; the last threads may have none
-            const int c = rank * cols + e % cols;
-            const int n = n0 + c;
-            if (n < g.N && c < kFewCols && e < per * cols) {
+            const int n = n0 + rank * cols + e % cols;
+            if (n < g.N) {
                 const float bias = g.bias != nullptr ? __bfloat162float(g.bias[n]) : 0.0f;
                 const float* p = parts + e % cols;
 #pragma unroll 4
-                for (int t = e / cols; t < rows; t += per) {
+                for (int t = e / cols; t < g.T; t += S) {
                     float v = p[t * cols];
 #pragma unroll
                     for (int q = 1; q < 8; ++q)
                         if (q < S) v += p[(q * TN + t) * cols];
-                    few_store(g, t0 + t, n, v, bias);
+                    few_store(g, t, n, v, bias);
                 }
             }
         }
