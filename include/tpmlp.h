@@ -162,8 +162,7 @@ tpmlp_status tp_linear_bwd(const void* dY, const void* X, const void* W, void* d
  * epilogue: H = X·W + bias, Y = act(H) + R. Arguments as tp_linear_fwd, plus:
  * act: TPMLP_ACT_NONE, TPMLP_GELU_ERF or TPMLP_GELU_TANH.
  * R: T×N of dtype dt, added after the activation, or NULL. R may be Y itself
- *   (the residual stream updated in place); no other output may overlap an
- *   input.
+ *   (the residual stream updated in place).
  * H: T×N output of dtype dt, the pre-activation the backward needs, or NULL
  *   (inference). With TPMLP_ACT_NONE it must be NULL.
  * Up to 128 rows (single tokens, small batches) the tensor-core path splits
@@ -180,7 +179,8 @@ tpmlp_status tp_linear_bwd(const void* dY, const void* X, const void* W, void* d
  * for invalid sizes). The forward needs them only where its schedule splits
  * tiles (never up to 128 rows, on the plain path or under split policy 1);
  * without them it then returns TPMLP_ERR_WORKSPACE. With T == 0, dW and dbias
- * are set to zero. */
+ * are set to zero. An output that overlaps an input or another output, but for
+ * R = Y, gives TPMLP_ERR_INVALID. */
 size_t tpmlp_linear_ex_workspace_size(int64_t T, int64_t K, int64_t N, int p, tpmlp_split split,
                                       tpmlp_dtype dt);
 tpmlp_status tp_linear_fwd_ex(const void* X, const void* W, const void* bias, const void* R, void* H,
@@ -211,7 +211,8 @@ tpmlp_status tp_linear_bwd_ex(const void* dY, const void* X, const void* W, cons
  * residual path around the block; adding it here saves a pass over dX. The
  * rows are summed in a fixed order. Needs tpmlp_layernorm_workspace_size()
  * bytes (0 for invalid sizes). With T == 0, dgamma and dbeta are set to zero.
- * No output may overlap an input, except that dX may be dY or dR itself. */
+ * dX may be dY or dR itself; any other output that overlaps an input or another
+ * output gives TPMLP_ERR_INVALID, forward and backward. */
 size_t tpmlp_layernorm_workspace_size(int64_t T, int64_t h, tpmlp_dtype dt);
 tpmlp_status tp_layernorm_fwd(const void* X, const void* gamma, const void* beta, void* Y, float* mean,
                               float* rstd, int64_t T, int64_t h, float eps, tpmlp_dtype dt,
@@ -275,7 +276,10 @@ tpmlp_status tp_mlp_recompute_hidden(const void* X, const void* A, const void* a
  *
  * tpmlp_ckpt8_encode writes C and S of a T×F matrix H of dtype dt (for
  * other activations a caller keeps); tpmlp_ckpt8_decode writes the values C
- * and S stand for as dtype dt (exact in either type). */
+ * and S stand for as dtype dt (exact in either type).
+ *
+ * In all four, an output that overlaps an input or another output, but for
+ * R = Z, gives TPMLP_ERR_INVALID. */
 size_t tpmlp_ckpt8_workspace_size(int64_t T, int64_t h, int64_t F, int p, tpmlp_dtype dt);
 tpmlp_status tp_mlp_fwd_ckpt8(const void* X, const void* A, const void* a, const void* B,
                               const void* b, const void* R, void* C, void* S, void* Y, void* Z,

@@ -22,6 +22,32 @@ bool known_grad(tpmlp_dtype g, tpmlp_dtype dt) { return g == TPMLP_FP32 || (g ==
 // Sizes that the kernels' 32-bit row and column indices hold, tiles' last rows included.
 bool fits32(int64_t x) { return x < (int64_t(1) << 31) - 1024; }
 
+// A matrix of a call, as bytes.
+struct Span {
+    const void* p;
+    int64_t bytes;
+};
+
+// Whether some output shares memory with an input or with another output
+// (null pointers share none). Products read their operands while other tiles of
+// the output are written, so such a call has no defined result.
+bool overlapping(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+    auto meet = [](const Span& a, const Span& b) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+        return a.p != nullptr && b.p != nullptr && x < y + static_cast<uintptr_t>(b.bytes) &&
+               y < x + static_cast<uintptr_t>(a.bytes);
+    };
+    for (const Span* o = outs.begin(); o != outs.end(); ++o) {
+        for (const Span& i : ins)
+            if (meet(*o, i)) return true;
+        for (const Span* q = o + 1; q != outs.end(); ++q)
+            if (meet(*o, *q)) return true;
+    }
+    return false;
+}
+
+int64_t size_of(tpmlp_dtype dt) { return dt == TPMLP_BF16 ? 2 : 4; }
+
 // ------------------------------------------------------------- plain products
 
 // One product, or two of the same kind in one launch (q may be null). Tiles
@@ -436,6 +462,10 @@ tpmlp_status linear_fwd_ex_impl(const void* X, const void* W, const void* bias, 
     if (T == 0) return TPMLP_OK;
     if (!X || !W || !Y) return TPMLP_ERR_INVALID;
     if (!fits32(T) || !fits32(K) || !fits32(N)) return TPMLP_ERR_UNSUPPORTED;
+    const int64_t es = size_of(dt);
+    if (overlapping({{Y, T * N * es}, {H, T * N * es}},
+                    {{X, T * K * es}, {W, K * N * es}, {bias, N * es}, {R == Y ? nullptr : R, T * N * es}}))
+        return TPMLP_ERR_INVALID;
     // the relaying activation epilogues run whole tiles (kSplittable)
     const SchedReq req = (act != TPMLP_ACT_NONE && K >= kRelayMinKAct) ? SchedReq{} : pl.fwd;
     const bool splits = pl.tc && T > kFewMaxRows && req.kind != SCHED_TILES;
@@ -750,6 +780,10 @@ tpmlp_status tp_layernorm_fwd(const void* X, const void* gamma, const void* beta
     if ((mean == nullptr) != (rstd == nullptr)) return TPMLP_ERR_INVALID;
     if (T > 0 && (!X || !Y)) return TPMLP_ERR_INVALID;
     if (!fits32(T) || !fits32(h)) return TPMLP_ERR_UNSUPPORTED;
+    const int64_t es = size_of(dt);
+    if (overlapping({{Y, T * h * es}, {mean, T * 4}, {rstd, T * 4}},
+                    {{X, T * h * es}, {gamma, h * es}, {beta, h * es}}))
+        return TPMLP_ERR_INVALID;
     TPMLP_TRY(check_device());
     if (T == 0) return TPMLP_OK;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -772,6 +806,11 @@ tpmlp_status tp_layernorm_bwd(const void* dY, const void* X, const void* gamma, 
     }
     if (workspace == nullptr || workspace_bytes < norm_workspace(T, h, dt)) return TPMLP_ERR_WORKSPACE;
     if (!aligned16(workspace)) return TPMLP_ERR_ALIGN;
+    const int64_t es = size_of(dt);
+    if (overlapping({{dX, T * h * es}, {dgamma, h * 4}, {dbeta, h * 4}},
+                    {{dX == dY ? nullptr : dY, T * h * es}, {X, T * h * es}, {gamma, h * es}, {mean, T * 4},
+                     {rstd, T * 4}, {dX == dR ? nullptr : dR, T * h * es}}))
+        return TPMLP_ERR_INVALID;
     if (dt == TPMLP_BF16)
         return norm_bwd_impl<bf16>(dY, X, gamma, mean, rstd, dR, dX, dgamma, dbeta, T, h, workspace, st);
     return norm_bwd_impl<float>(dY, X, gamma, mean, rstd, dR, dX, dgamma, dbeta, T, h, workspace, st);
@@ -816,6 +855,10 @@ tpmlp_status tp_linear_bwd_ex(const void* dY, const void* X, const void* W, cons
     if (!fits32(T) || !fits32(K) || !fits32(N) || !columns_ok(N) || !plain_grid_ok(K, N) ||
         !plain_grid_ok(T, K) || pl.chunks > kMaxGridY)
         return TPMLP_ERR_UNSUPPORTED;
+    const int64_t es = size_of(dt), eg = size_of(grad_dt);
+    if (overlapping({{dX, T * K * es}, {dW, K * N * eg}, {dbias, N * eg}, {dH, T * N * es}},
+                    {{dY, T * N * es}, {X, T * K * es}, {W, K * N * es}, {H, T * N * es}}))
+        return TPMLP_ERR_INVALID;
     if (dt == TPMLP_FP32)
         return linear_bwd_ex_run<float, float>(pl, dY, X, W, H, dX, dW, dbias, dH, T, K, N, act, workspace, st);
     if (grad_dt == TPMLP_BF16)
@@ -840,6 +883,11 @@ tpmlp_status tp_mlp_fwd_ckpt8(const void* X, const void* A, const void* a, const
         return TPMLP_ERR_WORKSPACE;
     if (!pl.fwd_split && !pl.fwd_dyn) workspace = nullptr;
     if (!aligned16(C)) return TPMLP_ERR_ALIGN;
+    const int64_t es = size_of(dt), blocks = c8_blocks(F);
+    if (overlapping({{C, T * blocks * kC8Block}, {S, T * blocks}, {Y, T * F * es}, {Z, T * h * es}},
+                    {{X, T * h * es}, {A, h * F * es}, {a, F * es}, {B, F * h * es}, {b, h * es},
+                     {R == Z ? nullptr : R, T * h * es}}))
+        return TPMLP_ERR_INVALID;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (pl.tc) {
         for (const void* q : {X, A, a, B, b, R, static_cast<const void*>(Y), static_cast<const void*>(Z)})
@@ -869,6 +917,12 @@ tpmlp_status tp_mlp_bwd_ckpt8(const void* dZ, const void* X, const void* A, cons
     }
     if (!dZ || !X || !A || !B || !C || !S || !dX || !dH || !Y) return TPMLP_ERR_INVALID;
     if (!aligned16(C)) return TPMLP_ERR_ALIGN;
+    const int64_t es = size_of(dt), eg = size_of(grad_dt), blocks = c8_blocks(F);
+    if (overlapping({{dX, T * h * es}, {dA, h * F * eg}, {da, F * eg}, {dB, F * h * eg}, {db, h * eg},
+                     {dH, T * F * es}, {Y, T * F * es}},
+                    {{dZ, T * h * es}, {X, T * h * es}, {A, h * F * es}, {B, F * h * es},
+                     {C, T * blocks * kC8Block}, {S, T * blocks}}))
+        return TPMLP_ERR_INVALID;
     if (pl.tc) {
         for (const void* q : {dZ, X, A, B, static_cast<const void*>(dX), static_cast<const void*>(dA),
                               static_cast<const void*>(da), static_cast<const void*>(dB),
@@ -891,9 +945,10 @@ tpmlp_status tpmlp_ckpt8_encode(const void* H, void* C, void* S, int64_t T, int6
     TPMLP_TRY(check_device());
     if (T == 0) return TPMLP_OK;
     if (!aligned16(C)) return TPMLP_ERR_ALIGN;
+    const int64_t es = size_of(dt), blocks = c8_blocks(F);
+    if (overlapping({{C, T * blocks * kC8Block}, {S, T * blocks}}, {{H, T * F * es}})) return TPMLP_ERR_INVALID;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const double esize = dt == TPMLP_BF16 ? 2.0 : 4.0;
-    return timed(K_C8, 0.0, (esize + 33.0 / 32.0) * T * F, st, [&] {
+    return timed(K_C8, 0.0, (es + 33.0 / 32.0) * T * F, st, [&] {
         return dt == TPMLP_BF16 ? ckpt8_encode_launch<bf16>(H, C, S, T, F, st)
                                 : ckpt8_encode_launch<float>(H, C, S, T, F, st);
     });
@@ -907,9 +962,10 @@ tpmlp_status tpmlp_ckpt8_decode(const void* C, const void* S, void* H, int64_t T
     TPMLP_TRY(check_device());
     if (T == 0) return TPMLP_OK;
     if (!aligned16(C)) return TPMLP_ERR_ALIGN;
+    const int64_t es = size_of(dt), blocks = c8_blocks(F);
+    if (overlapping({{H, T * F * es}}, {{C, T * blocks * kC8Block}, {S, T * blocks}})) return TPMLP_ERR_INVALID;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const double esize = dt == TPMLP_BF16 ? 2.0 : 4.0;
-    return timed(K_C8, 0.0, (esize + 33.0 / 32.0) * T * F, st, [&] {
+    return timed(K_C8, 0.0, (es + 33.0 / 32.0) * T * F, st, [&] {
         return dt == TPMLP_BF16 ? ckpt8_decode_launch<bf16>(C, S, H, T, F, st)
                                 : ckpt8_decode_launch<float>(C, S, H, T, F, st);
     });

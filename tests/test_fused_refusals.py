@@ -37,6 +37,18 @@ def test_layernorm_forward_refuses_sizes(lib, bad):
     assert norm_fwd(lib, **bad) == binding.ERR_UNSUPPORTED
 
 
+def test_layernorm_forward_refuses_overlap(lib):
+    """4 × 8 bf16: X at 4096..4160. An output that shares a byte with it, or with another output, is refused."""
+    at = ctypes.c_void_p
+    for y in (4096, 4096 - 63, 4096 + 63):
+        assert norm_fwd(lib, X=at(4096), Y=at(y), mean=at(8192), rstd=at(8208)) == binding.ERR_INVALID
+    assert norm_fwd(lib, X=at(4096), Y=at(256), mean=at(4156), rstd=at(8208)) == binding.ERR_INVALID
+    assert norm_fwd(lib, X=at(4096), Y=at(256), mean=at(8192), rstd=at(8204)) == binding.ERR_INVALID
+    if not torch.cuda.is_available():  # side by side is no overlap: the next refusal is the missing GPU
+        for y in (4096 - 64, 4096 + 64):
+            assert norm_fwd(lib, X=at(4096), Y=at(y), mean=at(8192), rstd=at(8208)) == binding.ERR_CUDA
+
+
 @pytest.mark.parametrize("i", range(9))
 def test_layernorm_backward_refuses_null(lib, i):
     args = [VP] * 9

@@ -220,3 +220,47 @@ def test_wrong_device_stream_is_refused():
 
     with pytest.raises(ValueError, match="stream"):
         binding.layernorm_forward(v["S"], v["gamma"], v["beta"], stream=Other())
+
+
+def test_overlapping_outputs_are_refused():
+    """An output that is an input, or shares memory with one, would be written while other rows are still read."""
+    T, h = 64, 128
+    g = torch.Generator(device="cuda").manual_seed(5)
+
+    def rand(*shape):
+        return torch.randn(*shape, generator=g, device="cuda").bfloat16()
+
+    X, W, b, R = rand(T, h), rand(h, h), rand(h), rand(T, h)
+    before = binding.launch_count()
+
+    def refused(f, *args, **kw):
+        with pytest.raises(binding.TPMLPError) as e:
+            f(*args, **kw)
+        assert e.value.status == binding.ERR_INVALID
+
+    both = rand(2 * T, h)
+    refused(binding.fused_linear_forward, X, W, b, residual=X, out=X)
+    refused(binding.fused_linear_forward, X, W, b, residual=both[:T], out=both[8:T + 8])
+    refused(binding.fused_linear_forward, X, W, b, activation="gelu", out=both[:T], hidden=both[1:T + 1])
+    refused(binding.fused_linear_backward, R, X, W, out=(R, None, None, None))
+    refused(binding.fused_linear_backward, R, X, W, rand(T, h), activation="gelu", out=(None, None, None, X))
+    refused(binding.layernorm_forward, X, b, b, out=(X, None, None))
+    mean, rstd = torch.zeros(T, device="cuda"), torch.ones(T, device="cuda")
+    refused(binding.layernorm_backward, R, X, b, mean, rstd, out=(X, None, None))
+    refused(binding.layernorm_backward, both[1:T + 1], X, b, mean, rstd, out=(both[:T], None, None))
+    refused(binding.forward_ckpt8, X, W, b, W, b, 2, residual=X, scratch=R, out=(None, None, R))
+    refused(binding.forward_ckpt8, X, W, b, W, b, 2, out=(None, None, X))
+    assert binding.launch_count() == before
+    C, S, Z = binding.forward_ckpt8(X, W, b, W, b, 2)
+    before = binding.launch_count()
+    for k in ("dX", "dH", "Y"):
+        refused(binding.backward_ckpt8, R, X, W, W, C, S, 2, out={k: R})
+    assert binding.launch_count() == before
+    # the allowed ones: the residual in place, a gradient in place
+    want = binding.fused_linear_forward(X, W, b, residual=R)
+    R2 = R.clone()
+    assert torch.equal(binding.fused_linear_forward(X, W, b, residual=R2, out=R2), want)
+    # neighbours in one buffer
+    buf = rand(2 * T, h)
+    buf[:T] = X
+    assert torch.equal(binding.fused_linear_forward(buf[:T], W, b, residual=R, out=buf[T:]), want)
