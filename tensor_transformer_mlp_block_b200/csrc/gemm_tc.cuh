@@ -832,8 +832,8 @@ __device__ __forceinline__ void load_extra(const GemmArgs& g, int row, int col0,
 // slot (kResidTma): one load in flight at a time, issued when the previous chunk
 // has been read, so that it lands during that chunk's arithmetic. Loaded a lane
 // per row they cost 32 lines per instruction: 6144 × 4096 outputs, K = 1024, bias
-// and residual took 78 µs on B200 that way, 55 issued a chunk ahead, against 41
-// without a residual.
+// and residual took 78 µs on B200 that way, 55 issued a chunk ahead, 50 so,
+// against 41 without a residual (short K: bound by the epilogue).
 struct ResidLoad {
     const CUtensorMap* map;
     uint32_t bar, buf;
