@@ -25,6 +25,23 @@ def test_encode_is_the_definition(T, F, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("F", [4, 36, 100, 252, 260, 516, 1004])
+def test_decode_by_width_and_alignment(F, dtype):
+    """Widths of whole 4, 8 or single elements, into aligned and unaligned rows; nothing beside them is written."""
+    T, dt = 67, DT[dtype]
+    g = torch.Generator(device="cuda").manual_seed(F)
+    H = torch.randn(T, F, generator=g, device="cuda").to(dt)
+    C, S = binding.ckpt8_encode(H)
+    want = eight_bit_values(C, S, F)
+    for off in (0, 1, 2, 4, 8):
+        buf = torch.full((T * F + 16,), 9.0, dtype=dt, device="cuda")
+        out = buf[off:off + T * F].view(T, F)
+        binding.ckpt8_decode(C, S, F, dtype=dt, out=out)
+        assert torch.equal(out.double(), want)
+        assert (buf[:off] == 9).all() and (buf[off + T * F:] == 9).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_encode_special_values(dtype):
     dt = DT[dtype]
     H = torch.zeros(14, 40, device="cuda", dtype=torch.float32)
