@@ -262,7 +262,10 @@ tpmlp_status tp_mlp_recompute_hidden(const void* X, const void* A, const void* a
  * accumulator), Y = act(H), Z = Σ Y_i·B_i + b + R. Arguments as
  * tp_mlp_fwd_ex, with C and S in place of H, and R: T×h of dtype dt, the
  * residual added to Z, or NULL (R may be Z itself). Y (T×F) holds the
- * activation on return; the backward does not need it.
+ * activation on return; the backward does not need it. With TPMLP_BF16 the sums
+ * are the tensor cores', whose fp32 accumulation truncates (up to K/16 times
+ * 2^-25 of a sum over K), so a value that close to halfway between two integers
+ * may get either.
  *
  * tp_mlp_bwd_ckpt8: with H̃ the values C and S stand for, dH = (dZ·Bᵀ) ⊙
  * act′(H̃), Y = act(H̃) (rebuilt, written to Y, T×F), dB = Yᵀ·dZ, dA = Xᵀ·dH,
