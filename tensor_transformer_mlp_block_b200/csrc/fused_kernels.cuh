@@ -438,6 +438,7 @@ __global__ void __launch_bounds__(BT == 128 ? 256 : 128, BT == 128 ? 2 : 4)
         }
     };
     const int n_steps = kend > kbeg ? (kend - kbeg + BK - 1) / BK : 0;
+    if constexpr (SPLIT && sizeof(TI) != 4) cluster_arrive();
     if constexpr (sizeof(TI) == 4) {
         float4 ra[TiledOperand<TI, BT>::PER / 4], rb[TiledOperand<TI, BT>::PER / 4];
 #pragma unroll
@@ -495,8 +496,12 @@ __global__ void __launch_bounds__(BT == 128 ? 256 : 128, BT == 128 ? 2 : 4)
         float* parts = &sA[0][0][0];
         static_assert(sizeof(sA) >= 64 * 64 * 4 || sizeof(TI) != 4, "parts fit the A ring");
         __shared__ __align__(16) float own_parts[sizeof(TI) == 4 ? 1 : 64 * 64];
-        if constexpr (sizeof(TI) != 4) parts = own_parts;
-        else cluster_sync();
+        if constexpr (sizeof(TI) != 4) {
+            parts = own_parts;
+            cluster_wait();  // the other blocks have started
+        } else {
+            cluster_sync();
+        }
         const int own = 64 / S;  // rows per block; S divides 64
 #pragma unroll
         for (int i = 0; i < 4; ++i) {

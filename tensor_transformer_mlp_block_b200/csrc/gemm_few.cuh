@@ -116,6 +116,7 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<TN>::CTAS)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    if (S > 1) cluster_arrive();  // this CTA has started (waited for before the sums are pushed)
     grid_dep_wait();
     grid_dep_launch();
     const uint64_t limit = g.wait_limit_ns;
@@ -153,6 +154,7 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<TN>::CTAS)
             }
         }
         __syncwarp();
+        if (S > 1) cluster_wait();
     } else if (warp == 1) {
         if (lane == 0) {
             for (int kb = kb0; kb < kb1; ++kb) {
@@ -175,6 +177,7 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<TN>::CTAS)
             mbar_wait_bounded(smem_u32(done), 0, &never, limit);
         }
         __syncwarp();
+        if (S > 1) cluster_wait();
     } else {
         const int quad = warp & 3;
         const int c = quad * 32 + lane;  // column of W within the tile
@@ -188,6 +191,7 @@ __global__ void __launch_bounds__(kFewThreads, FewCfg<TN>::CTAS)
         ok = mbar_wait_bounded(smem_u32(done), 0, abort, limit);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) raise_timeout(abort);
+        if (S > 1) cluster_wait();  // the other CTAs have started
         if (ok) {
             tc_fence_after();
             const int n = n0 + c;

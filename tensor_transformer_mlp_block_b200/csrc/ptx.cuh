@@ -321,6 +321,16 @@ __device__ __forceinline__ void cluster_sync() {
                      : "memory");
 }
 
+// The same in two halves, each called once by every thread: a CTA's shared memory
+// may be written by another only once it has started, and its arrival tells that.
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 // Address of the same shared-memory location in CTA `rank` of the cluster.
 __device__ __forceinline__ uint32_t mapa_shared(uint32_t addr, uint32_t rank) {
     uint32_t r;
