@@ -157,7 +157,7 @@ struct TileCfg {
     static constexpr int STAGES = (196608 / STAGE_BYTES) > 8 ? 8 : (196608 / STAGE_BYTES);
     // tensor-memory columns: two accumulators, rounded up to a power of two
     static constexpr int TMEM_COLS = (2 * BN <= 128) ? 128 : (2 * BN <= 256 ? 256 : 512);
-    static constexpr int BAR_BYTES = 8 * (2 * STAGES + 5 + 8) + 16 + 8 * kEpiWarps;  // the last: residual loads
+    static constexpr int BAR_BYTES = 8 * (2 * STAGES + 5 + 8) + 16 + 16 * kEpiWarps;  // the last: residual loads
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + kEpiStagingBytes + BAR_BYTES;
 };
 
@@ -833,10 +833,14 @@ __device__ __forceinline__ void load_extra(const GemmArgs& g, int row, int col0,
 // has been read, so that it lands during that chunk's arithmetic. Loaded a lane
 // per row they cost 32 lines per instruction: 6144 × 4096 outputs, K = 1024, bias
 // and residual took 78 µs on B200 that way, 55 issued a chunk ahead, 50 so,
-// against 41 without a residual (short K: bound by the epilogue).
+// against 41 without a residual (short K: bound by the epilogue). The buffer is
+// read with ordinary loads and written by the TMA: a warp barrier does not order
+// the two (the loads may still wait for shared memory, which the tensor core's
+// operands keep busy), so every lane arrives on a second mbarrier after its loads
+// and the next load is issued once all have.
 struct ResidLoad {
     const CUtensorMap* map;
-    uint32_t bar, buf;
+    uint32_t bar, freed, buf;
     uint32_t phase;
     bool on, in_flight;
 
@@ -854,12 +858,13 @@ struct ResidLoad {
         if (!on) return true;
         const bool got = mbar_wait_bounded(bar, phase, abort, limit);
         if (!__all_sync(0xffffffffu, got)) return false;
-        phase ^= 1u;
         in_flight = false;
 #pragma unroll
         for (int q = 0; q < 4; ++q) ex[q] = ld_shared_v4(buf + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4));
-        __syncwarp();
-        return true;
+        mbar_arrive(freed);
+        const bool free = mbar_wait_bounded(freed, phase, abort, limit);
+        phase ^= 1u;
+        return __all_sync(0xffffffffu, free);
     }
 };
 
@@ -1129,9 +1134,10 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& g, const CUtensorM
         tma_prefetch_desc(tmO0);
         if (EpiTraits<EPI>::kTwo || EpiTraits<EPI>::kResidTma || g.second) tma_prefetch_desc(tmO1);
     }
-    ResidLoad resid{tmO1, 0u, slot + 2048, 0u, false, false};
+    ResidLoad resid{tmO1, 0u, 0u, slot + 2048, 0u, false, false};
     if constexpr (EpiTraits<EPI>::kResidTma) {
         resid.bar = smem_u32(&rbars[warp - 2]);
+        resid.freed = smem_u32(&rbars[kEpiWarps + warp - 2]);
         resid.on = g.resid != nullptr;
     }
     uint32_t xcount = 0;
@@ -1432,7 +1438,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         if constexpr (EpiTraits<EPI>::kResidTma)
-            for (int x = 0; x < kEpiWarps; ++x) mbar_init(smem_u32(&rbars[x]), 1);
+            for (int x = 0; x < kEpiWarps; ++x) {
+                mbar_init(smem_u32(&rbars[x]), 1);
+                mbar_init(smem_u32(&rbars[kEpiWarps + x]), 32);
+            }
         for (int x = 0; x < 4; ++x) {
             mbar_init(smem_u32(&xfull[x]), 32);
             mbar_init(smem_u32(&xempty[x]), 32);

@@ -37,7 +37,7 @@ struct Tile2Cfg {
     // barriers: ring (2·STAGES), accumulators (4), drain, relay (8), item
     // queue (2·kQueue); then the TMEM address, the abort flag, the queue's items,
     // and the epilogue warps' residual loads
-    static constexpr int BAR_BYTES = 8 * (2 * STAGES + 5 + 8 + 2 * kQueue) + 16 + 4 * kQueue + 8 * kEpiWarps;
+    static constexpr int BAR_BYTES = 8 * (2 * STAGES + 5 + 8 + 2 * kQueue) + 16 + 4 * kQueue + 16 * kEpiWarps;
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + STAGING_BYTES + BAR_BYTES;
 };
 
@@ -89,7 +89,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
     if (threadIdx.x == 0) {
         if constexpr (EpiTraits<EPI>::kResidTma)
-            for (int x = 0; x < kEpiWarps; ++x) mbar_init(smem_u32(&rbars[x]), 1);
+            for (int x = 0; x < kEpiWarps; ++x) {
+                mbar_init(smem_u32(&rbars[x]), 1);
+                mbar_init(smem_u32(&rbars[kEpiWarps + x]), 32);
+            }
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(smem_u32(&full[s]), 1);
             mbar_init(smem_u32(&empty[s]), 1);

@@ -175,6 +175,23 @@ def test_long_product_variant():
     check_forward(v, "none", R)
 
 
+@pytest.mark.parametrize("T,K,N", [(8200, 4096, 2568), (6144, 1024, 2048), (1777, 4096, 1032)])
+@pytest.mark.parametrize("act", ["none", "gelu"])
+def test_residual_is_the_same_every_time(T, K, N, act):
+    """The residual's buffer is read and loaded again many times over; every run gives the first one's bits, and
+    those are right."""
+    v = make(T, K, N, "bf16", seed=3)
+    want = binding.fused_linear_forward(v["X"], v["W"], v["bias"], activation=act, residual=v["R"])
+    check_forward(v, act, want)
+    got, bad = torch.empty_like(want), torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(150):
+        got.fill_(9.0)
+        binding.fused_linear_forward(v["X"], v["W"], v["bias"], activation=act, residual=v["R"], out=got)
+        bad += (got != want).sum()
+    assert int(bad) == 0
+    assert binding.last_device_status() == binding.OK
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 def test_offsets_past_32_bits(dtype):
     """More than 2^31 outputs: the last rows come out right."""
