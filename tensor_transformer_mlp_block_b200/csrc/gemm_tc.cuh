@@ -1240,6 +1240,14 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& g, const CUtensorM
                         raise_timeout(abort);
                         break;
                     }
+                    if constexpr (EpiTraits<EPI>::kResidTma) {
+                        // The residual is loaded (async proxy) over the half of
+                        // the slot that this warp's lanes filled with ordinary
+                        // stores for those chunks: every lane orders its stores
+                        // before the load that lane 0 issues.
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
                 }
                 float csx[32];  // unused: no column sums on split tiles
                 bool split_failed = false;
