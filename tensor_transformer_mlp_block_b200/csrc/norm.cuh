@@ -283,8 +283,12 @@ __global__ void __launch_bounds__(512) norm_bwd_kernel(const T* dY, const T* __r
 // warp, or the block) owns a ring and walks the rows group, group + groups, ...;
 // a row's stage is refilled after the next row's sums, whose barrier tells that
 // every thread is through with it (with one stage, after a barrier of its own).
-// KEEP: x̂ and dY ⊙ gamma stay in registers
-// between the two uses, up to 16 elements per thread. ONE: one stage, gamma read
+// In a warp's ring a vote stands for that barrier. A vote orders no memory, so it
+// serves only because what a lane reads of a stage is used before: x and dY in the
+// sums that the warp has exchanged, dR in the dX it has stored. No read can still
+// be under way when lane 0 issues the refill.
+// KEEP: x̂ and dY ⊙ gamma stay in registers between the two uses, up to 16
+// elements per thread (a warp's ring needs it: see above). ONE: one stage, gamma read
 // from global memory (rows so wide that no more fits). Waits are bounded.
 struct NormRing {
     int stages;  // rows a group's ring holds (1..8)
@@ -299,6 +303,7 @@ __global__ void __launch_bounds__(MAX_THREADS, PER_SM) norm_bwd_ring_kernel(cons
                                                             float* __restrict__ part_g,
                                                             float* __restrict__ part_b, int64_t R, int h,
                                                             NormRing ring) {
+    static_assert(KEEP || !WARP, "a warp's refill relies on x and dY being used up by the vote");
     constexpr int VE = 16 / sizeof(T), PV = VE / 2;
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ float red[2][2][32];
