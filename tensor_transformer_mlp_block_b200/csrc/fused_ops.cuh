@@ -879,6 +879,11 @@ tpmlp_status tp_mlp_fwd_ckpt8(const void* X, const void* A, const void* a, const
     TPMLP_TRY(c8_checks(T, h, F, p, dt, act, &pl, workspace, workspace_bytes, false));
     if (T == 0) return TPMLP_OK;
     if (!X || !A || !B || !C || !S || !Y || !Z) return TPMLP_ERR_INVALID;
+    // up to kFewMaxRows rows the second product is the few-row kernel's, which splits no tiles
+    if (pl.tc && T <= kFewMaxRows) {
+        pl.f2 = SchedReq{};
+        pl.fwd_split = pl.f1.kind != SCHED_TILES;
+    }
     if ((pl.fwd_split || pl.fwd_dyn) && (workspace == nullptr || workspace_bytes < pl.total))
         return TPMLP_ERR_WORKSPACE;
     if (!pl.fwd_split && !pl.fwd_dyn) workspace = nullptr;
