@@ -157,7 +157,7 @@ struct TileCfg {
     static constexpr int STAGES = (196608 / STAGE_BYTES) > 8 ? 8 : (196608 / STAGE_BYTES);
     // tensor-memory columns: two accumulators, rounded up to a power of two
     static constexpr int TMEM_COLS = (2 * BN <= 128) ? 128 : (2 * BN <= 256 ? 256 : 512);
-    static constexpr int BAR_BYTES = 8 * (2 * STAGES + 5 + 8) + 16 + 16 * kEpiWarps;  // the last: residual loads
+    static constexpr int BAR_BYTES = 8 * (2 * STAGES + 5 + 8) + 16;
     static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + kEpiStagingBytes + BAR_BYTES;
 };
 
@@ -1119,6 +1119,8 @@ __device__ __forceinline__ void epilogue_role(const GemmArgs& g, const CUtensorM
                                               volatile int* abort, uint64_t limit, int warp,
                                               int lane, const PairQueue* queue = nullptr,
                                               uint64_t* rbars = nullptr) {
+    // (up to 128 rows these epilogues' products are gemm_few.cuh's)
+    static_assert(PAIR || !EpiTraits<EPI>::kResid, "the residual's epilogues run on CTA pairs");
     constexpr int kChunks = BN / 64;  // 32-column chunks per half of the tile
     const int quad = warp & 3;          // tensor-memory lanes this warp may access
     const int half = (warp - 2) / 4;    // which half of the tile's columns
@@ -1439,17 +1441,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t* xempty = bars + 2 * STAGES + 9;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 2 * STAGES + 13);
     volatile int* abort = reinterpret_cast<volatile int*>(tmem_slot + 1);
-    uint64_t* rbars = reinterpret_cast<uint64_t*>(tmem_slot + 4);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        if constexpr (EpiTraits<EPI>::kResidTma)
-            for (int x = 0; x < kEpiWarps; ++x) {
-                mbar_init(smem_u32(&rbars[x]), 1);
-                mbar_init(smem_u32(&rbars[kEpiWarps + x]), 32);
-            }
         for (int x = 0; x < 4; ++x) {
             mbar_init(smem_u32(&xfull[x]), 32);
             mbar_init(smem_u32(&xempty[x]), 32);
@@ -1618,8 +1614,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else {
         // ------------------------------------------------ epilogue warps
         epilogue_role<BN, EPI, false, RELAY>(g, &tmO0, &tmO1, tmem_base, tfull, tempty, xfull, xempty, sEpi,
-                                             blockIdx.x, gridDim.x, kBM, 0, abort, limit, warp, lane, nullptr,
-                                             rbars);
+                                             blockIdx.x, gridDim.x, kBM, 0, abort, limit, warp, lane);
     }
 
     tc_fence_before();
