@@ -125,14 +125,14 @@ __global__ void __launch_bounds__(256) colsum_partial2_kernel(const T* __restric
         colsum_partial_block<T, VEC>(X2, R, C2, rows_per_chunk, partial2, bx - nb1, by);
 }
 
+__device__ __forceinline__ void store_f32(float* p, float v) { *p = v; }
+__device__ __forceinline__ void store_f32(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
+
 // Column sums, pass 2: out[c] = Σ over chunks of partial[chunk][c]. Block
 // (32, 8): x picks one of 32 consecutive columns (coalesced reads), y one of 8
 // contiguous chunk groups; each thread adds its group's chunks in ascending
 // order, then the 8 group sums are added in ascending group order. Fixed
 // assignment and order: bit-reproducible.
-__device__ __forceinline__ void store_f32(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_f32(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
-
 template <typename O>
 __device__ __forceinline__ void colsum_final_block(const float* __restrict__ partial, int chunks,
                                                    int64_t C, O* __restrict__ out, int64_t bx) {

@@ -354,9 +354,9 @@ tpmlp_status norm_bwd_impl(const void* dY, const void* X, const void* gamma, con
 
 // CTAs of a cluster that share a tile's K range (gemm_few.cuh): the power of
 // two up to 8 that fills the resident CTAs without a second wave and leaves
-// each at least two k-blocks. An SM streams about 64 GB/s however much its
-// ring holds, so what counts is that all of them load. Measured on B200 (µs,
-// S = 1 / 2 / 4 / 8): 24 rows, 16384 → 4096 (32 tiles) 82 / 45 / 27 / 24; 1
+// each at least two k-blocks. A CTA alone on its SM streams 44 to 51 GB/s (the
+// S = 1 times below), however much its ring holds, so what counts is that all
+// SMs load. Measured on B200 (µs, S = 1 / 2 / 4 / 8): 24 rows, 16384 → 4096 (32 tiles) 82 / 45 / 27 / 24; 1
 // row, 4096 → 16384 (128 tiles) 24.0 / 23.9 / 27 / 34; 16 rows, 4096 → 1024
 // (8 tiles) 23 / 14 / 8.5 / 5.9. Clusters of 3, 5, 6 or 7 leave SMs idle and
 // gain nothing (1 row, 12288 → 12288: S = 2 52, S = 3 66).
