@@ -167,7 +167,10 @@ tpmlp_status tp_linear_bwd(const void* dY, const void* X, const void* W, void* d
  *   (inference). With TPMLP_ACT_NONE it must be NULL.
  * Up to 128 rows (single tokens, small batches) the tensor-core path splits
  * K over a cluster of CTAs, so that reading W uses the whole GPU; K is then
- * summed in up to 8 consecutive parts, whatever the split policy.
+ * summed in up to 8 consecutive parts, whatever the split policy. With
+ * TPMLP_ACT_NONE and R = NULL this is tp_linear_fwd's product (its sums in
+ * another order), which under that name takes up to three times as long there
+ * and three to six times as long in fp32.
  *
  * Backward, for the upstream gradient dY (T×N; R's gradient is dY itself):
  *   dH = dY ⊙ act′(H)        (T×N, dtype dt, rounded once; written to dH)
@@ -269,7 +272,9 @@ tpmlp_status tp_mlp_recompute_hidden(const void* X, const void* A, const void* a
  *
  * tp_mlp_bwd_ckpt8: with H̃ the values C and S stand for, dH = (dZ·Bᵀ) ⊙
  * act′(H̃), Y = act(H̃) (rebuilt, written to Y, T×F), dB = Yᵀ·dZ, dA = Xᵀ·dH,
- * dX = Σ dH_i·A_iᵀ, da = 1ᵀ·dH, db = 1ᵀ·dZ. R's gradient is dZ itself.
+ * dX = Σ dH_i·A_iᵀ, da = 1ᵀ·dH, db = 1ᵀ·dZ. R's gradient is dZ itself. With
+ * TPMLP_BF16, Y and dH are rounded once and the sums that use them, da's too,
+ * are of the rounded values (as in tp_mlp_bwd).
  * Arguments as tp_mlp_bwd_ex; dA, da, dB and db have the type grad_dt:
  * TPMLP_FP32, or dt for gradients held in the weights' type.
  * The backward needs tpmlp_ckpt8_workspace_size() bytes (0 for invalid

@@ -393,7 +393,9 @@ def linear_workspace_size(T: int, K: int, N: int, p: int, split: str,
 
 def linear_forward(X, W, bias, p: int, split: str, *, out=None, workspace=None, stream=None):
     """Y = X·W + bias with W split into p shards by "columns" (QKV-style) or
-    "rows" (output-projection style). X: T×K, W: K×N, bias: N or None."""
+    "rows" (output-projection style). X: T×K, W: K×N, bias: N or None.
+    fused_linear_forward computes the same (its sums in another order) and is
+    the faster one up to 128 rows and in fp32."""
     T, K = X.shape
     N = W.shape[1]
     dt, dev = X.dtype, X.device
@@ -480,7 +482,10 @@ def recompute_activation(H, *, out=None, activation: str = "gelu", stream=None):
 # ------------------------------------------------- the pre-norm block's operators
 # Outputs and workspaces that these functions allocate belong to the stream the
 # kernels run on (`stream`, or the device's current one), so that the memory is
-# neither reused early nor still in use by other work.
+# neither reused early nor still in use by other work. Without `workspace` a call
+# allocates what it needs, which for most forward calls is nothing; one that is
+# given has the bytes that the operator's *_workspace_size function states,
+# whether or not the call uses them.
 
 class _Here:
     def __enter__(self):

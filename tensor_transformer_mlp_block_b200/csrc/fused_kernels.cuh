@@ -66,8 +66,11 @@ __device__ __forceinline__ void store8(T* p, int64_t c, int64_t n, const float* 
 // dH = dY ⊙ act′(H) and the partial column sums of dH before it is rounded:
 // one pass over dY and H. Grid (row chunks, ⌈C/256⌉), block (32, 8) as
 // colsum_partial_block: lane x holds columns [by·256 + 8x, +8), phase y the rows
-// chunk_begin + y, +8, ...; the 8 phases are added in order. 6144 × 4096 bf16 on
-// B200: 32 µs (4.7 TB/s; 23 µs at the copy rate), bound by the derivative's
+// chunk_begin + y, +8, ...; the 8 phases are added in order. dH is rounded to
+// dY's type because both products take it as a tensor-core operand, bf16 by bf16:
+// bf16 gradients are then 2.35e-3 off (2-norm), where rounding them alone is
+// 1.66e-3; keeping dH whole would take it in two parts and twice the products.
+// 6144 × 4096 bf16 on B200: 32 µs (4.7 TB/s; 23 µs at the copy rate), bound by the derivative's
 // arithmetic beside the loads.
 template <typename T, bool TANH, bool VEC>
 __global__ void __launch_bounds__(256) act_grad_kernel(const T* __restrict__ dY, const T* __restrict__ H,
@@ -135,8 +138,9 @@ __global__ void __launch_bounds__(256) act_grad_kernel(const T* __restrict__ dY,
 // a lane holds 8 columns, so 4 lanes share a block and exchange its maximum in
 // two steps. The tile's 256 scale bytes are gathered in shared memory and written
 // 32 to a row of S (one row of the tile each would touch a 32-byte sector per
-// byte). Encoding 8192 × 16384 takes 96 µs in bf16 (4.2 TB/s: bound by the
-// arithmetic per element) and 101 µs in fp32 (6.7 TB/s, the copy rate).
+// byte). Encoding 8192 × 16384 takes 96 µs in bf16 (4.2 TB/s: half of the issue
+// slots busy, the rest waiting for a lane's four loads) and 101 µs in fp32
+// (6.7 TB/s, the copy rate).
 
 // H to C and S.
 template <typename T, bool VEC>
